@@ -48,6 +48,24 @@ class pi_expert_weights(ctypes.Structure):
                 ("s_U", ctypes.c_void_p), ("s_V", ctypes.c_void_p)]
 
 
+class pi_attn_desc(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("cache_dtype", ctypes.c_int), ("page_size", ctypes.c_int), ("layout", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("rotary_pairs", ctypes.c_int), ("rope_theta", ctypes.c_float),
+                ("norm_eps", ctypes.c_float), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int), ("device", ctypes.c_int)]
+
+
+class _kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int)]
+
+
+class _kv_table(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_seqs", ctypes.c_int), ("width", ctypes.c_int),
+                ("stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -59,7 +77,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m activation_sparse_decode_threshold_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
-        vp, ip = ctypes.c_void_p, ctypes.c_int
+        vp, ip, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
         sigs = {
             "pi_ffn_create": [ctypes.POINTER(pi_ffn_desc), ctypes.POINTER(vp)],
             "pi_ffn_load_layer": [vp, ip, ctypes.POINTER(pi_expert_weights), vp, vp, vp],
@@ -77,6 +95,13 @@ def lib() -> ctypes.CDLL:
             "pi_debug_set": [vp, ip, ctypes.c_double],
             "pi_debug_phase_times": [vp, vp],
             "pi_predict_noalloc": [ip, ip, ip, ip, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp],
+            "pi_int4_create": [ip, ip, vp, vp, ip, vp, ctypes.POINTER(vp)],
+            "pi_int4_matvec": [vp, ip, ip, vp, i64, vp, ip, vp, i64, ctypes.c_float, vp],
+            "pi_attn_create": [ctypes.POINTER(pi_attn_desc), ctypes.POINTER(vp)],
+            "pi_attn_sync": [vp, vp],
+            "pi_kv_append": [vp, vp, vp, ip, vp, vp, ip, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp],
+            "pi_kv_read": [vp, vp, vp, ip, vp, vp, ip, vp, vp, vp],
+            "pi_paged_attention": [vp, vp, vp, vp, ip, vp, i64, vp, i64, vp, vp],
         }
         for name, args in sigs.items():
             f = getattr(L, name)
@@ -84,8 +109,9 @@ def lib() -> ctypes.CDLL:
             f.restype = ctypes.c_int
         L.pi_last_error.argtypes = []
         L.pi_last_error.restype = ctypes.c_char_p
-        L.pi_ffn_destroy.argtypes = [vp]
-        L.pi_ffn_destroy.restype = None
+        for name in ("pi_ffn_destroy", "pi_int4_destroy", "pi_attn_destroy"):
+            getattr(L, name).argtypes = [vp]
+            getattr(L, name).restype = None
         _lib = L
     return _lib
 
@@ -238,3 +264,213 @@ def pi_predict_noalloc(d_model, d_ff, rank, pred_dtype, threshold, V, U, bias, x
     _check(lib().pi_predict_noalloc(d_model, d_ff, rank, DTYPE[pred_dtype], threshold, _ptr(V), _ptr(U),
                                     _ptr(bias), _ptr(x), _ptr(idx), _ptr(count), _ptr(z), _stream(stream)),
            "pi_predict_noalloc")
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a decode layer.  Shapes, row distances and types come
+# from the tensors, so these wrappers check that the tensors are what the C
+# entry point will take them for; a mismatch raises PI_ERR_INVALID_ARG.
+# ---------------------------------------------------------------------------
+KV_LAYOUT = {"hnd": 0, "nhd": 1}
+_desc: dict = {}     # handle -> what the checks need of it
+
+
+def _require(ok, where: str, msg: str):
+    if not ok:
+        raise PiError(PI_ERR_INVALID_ARG, where, msg)
+
+
+def _float_code(t, where: str, name: str) -> int:
+    code = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}.get(str(t.dtype))
+    _require(code is not None, where, f"{name} must be float32, float16 or bfloat16")
+    return code
+
+
+def _on(device: int, where: str, **tensors):
+    for name, t in tensors.items():
+        _require(t is None or (t.is_cuda and t.device.index == device), where, f"{name} is not on cuda:{device}")
+
+
+def _int32(where: str, **tensors):
+    for name, t in tensors.items():
+        _require(t is None or str(t.dtype) == "torch.int32", where, f"{name} must be int32")
+
+
+def _stream_on(stream, device: int):
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def _handle_desc(h, kind: str, where: str):
+    d = _desc.get(h)
+    _require(d is not None and d["kind"] == kind, where, f"not a live {kind} handle")
+    return d
+
+
+def pi_int4_create(q, s, device=None, stream=None) -> int:
+    """`q`: uint8 [n_rows x n_cols/2] nibbles, `s`: float16 [n_rows x n_cols/32], both contiguous on the device."""
+    w = "pi_int4_create"
+    _require(q.is_cuda and s.is_cuda, w, "q and s must be CUDA tensors")
+    device = q.device.index if device is None else device
+    _on(device, w, q=q, s=s)
+    _require(q.dim() == 2 and str(q.dtype) == "torch.uint8" and q.is_contiguous(), w, "q must be contiguous uint8 [n, k/2]")
+    n, k = q.shape[0], 2 * q.shape[1]
+    _require(str(s.dtype) == "torch.float16" and s.is_contiguous() and tuple(s.shape) == (n, k // 32) and k % 32 == 0, w,
+             "s must be contiguous float16 [n, k/32]")
+    h = ctypes.c_void_p()
+    _check(lib().pi_int4_create(n, k, _ptr(q), _ptr(s), device, _stream_on(stream, device), ctypes.byref(h)), w)
+    _desc[h.value] = {"kind": "int4", "n": n, "k": k, "device": device}
+    return h.value
+
+
+def pi_int4_destroy(m: int):
+    if m and _desc.pop(m, None):
+        lib().pi_int4_destroy(m)
+
+
+def _token_rows(t, where: str, name: str, tokens: int, *shape):
+    """Row distance of a [tokens, ...] tensor whose rows are contiguous."""
+    _require(tuple(t.shape) == (tokens, *shape), where, f"{name} must be {[tokens, *shape]}, not {list(t.shape)}")
+    want = 1
+    for n, st in zip(reversed(shape), reversed(t.stride()[1:])):
+        _require(n == 1 or st == want, where, f"{name}: a token's values must be contiguous")
+        want *= n
+    return t.stride(0)
+
+
+def pi_int4_matvec(m, x, y, add=None, norm_eps=0.0, stream=None):
+    """y [tokens x n_rows] = add + W f(x), x [tokens x n_cols]."""
+    w = "pi_int4_matvec"
+    d = _handle_desc(m, "int4", w)
+    _on(d["device"], w, x=x, y=y, add=add)
+    tokens = x.shape[0]
+    xs, ys = _token_rows(x, w, "x", tokens, d["k"]), _token_rows(y, w, "y", tokens, d["n"])
+    if add is not None:
+        _require(add.dtype == y.dtype and (_token_rows(add, w, "add", tokens, d["n"]) == ys or tokens == 1), w,
+                 "add must have y's type and row distance")
+    _check(lib().pi_int4_matvec(m, tokens, _float_code(x, w, "x"), _ptr(x), xs, _ptr(add), _float_code(y, w, "y"),
+                                _ptr(y), ys, norm_eps, _stream_on(stream, d["device"])), w)
+
+
+def pi_attn_create(n_heads, n_kv_heads, head_dim, cache_dtype="bf16", page_size=64, layout="hnd", rotary_dim=0,
+                   rotary_pairs=False, rope_theta=10000.0, norm_eps=0.0, scale=0.0, softcap=0.0, window=0,
+                   device=0) -> int:
+    w = "pi_attn_create"
+    code = {"i8": DTYPE["i8row"]}.get(cache_dtype, DTYPE.get(cache_dtype))
+    _require(code is not None, w, f"unknown cache_dtype {cache_dtype!r}")
+    _require(layout in KV_LAYOUT, w, f"unknown layout {layout!r}")
+    desc = pi_attn_desc(n_heads, n_kv_heads, head_dim, code, page_size, KV_LAYOUT[layout], rotary_dim, int(rotary_pairs),
+                        rope_theta, norm_eps, scale, softcap, window, device)
+    h = ctypes.c_void_p()
+    _check(lib().pi_attn_create(ctypes.byref(desc), ctypes.byref(h)), w)
+    _desc[h.value] = {"kind": "attention", "heads": n_heads, "kv_heads": n_kv_heads, "dim": head_dim, "code": code,
+                      "page": page_size, "layout": layout, "device": device}
+    return h.value
+
+
+def pi_attn_destroy(a: int):
+    if a and _desc.pop(a, None):
+        lib().pi_attn_destroy(a)
+
+
+def pi_attn_sync(a, stream=None) -> int:
+    """Returns the status (does not raise): PI_ERR_DEVICE_CHECK after an index out of range."""
+    return lib().pi_attn_sync(a, _stream_on(stream, _handle_desc(a, "attention", "pi_attn_sync")["device"]))
+
+
+class pi_kv_cache:
+    """The tensors of one layer's cache: k and v [pages, kv heads, page size, row] ("hnd") or [pages, page size, kv
+    heads, row] ("nhd") with row = head_dim values (float16, bfloat16, int8) or head_dim/2 bytes (int4g32: uint8);
+    scales without the row (float32) for int8, with head_dim/32 float16 for int4g32."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.c = _kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
+        self.checked = None
+
+
+def _cache_arg(cache, d, where):
+    if cache.checked is not d:
+        row, dt, scale = {1: (d["dim"], "torch.float16", None), 2: (d["dim"], "torch.bfloat16", None),
+                          4: (d["dim"], "torch.int8", ((), "torch.float32")),
+                          3: (d["dim"] // 2, "torch.uint8", ((d["dim"] // 32,), "torch.float16"))}[d["code"]]
+        lead = (cache.k.shape[0], d["kv_heads"], d["page"]) if d["layout"] == "hnd" else \
+            (cache.k.shape[0], d["page"], d["kv_heads"])
+        for name in ("k", "v"):
+            t, s = getattr(cache, name), getattr(cache, name + "_scale")
+            _require(tuple(t.shape) == (*lead, row) and str(t.dtype) == dt and t.is_contiguous(), where,
+                     f"cache {name} must be contiguous {dt} {[*lead, row]}")
+            if scale is None:
+                _require(s is None, where, f"a cache of {dt} has no scales")
+            else:
+                _require(s is not None and tuple(s.shape) == (*lead, *scale[0]) and str(s.dtype) == scale[1]
+                         and s.is_contiguous(), where, f"cache {name}_scale must be contiguous {scale[1]} {[*lead, *scale[0]]}")
+            _on(d["device"], where, **{name: t, name + "_scale": s})
+        cache.checked = d
+    return ctypes.byref(cache.c)
+
+
+def _table_arg(table, d, where):
+    _int32(where, table=table)
+    _on(d["device"], where, table=table)
+    _require(table.dim() == 2 and (table.stride(1) == 1 or table.shape[1] == 1), where,
+             "table must be [sequences, pages] with contiguous rows")
+    return ctypes.byref(_kv_table(_ptr(table), table.shape[0], table.shape[1], table.stride(0)))
+
+
+def _places(where, d, pos, seq):
+    _int32(where, pos=pos, seq=seq)
+    _on(d["device"], where, pos=pos, seq=seq)
+    for name, t in (("pos", pos), ("seq", seq)):
+        _require(t is None or (t.dim() == 1 and t.shape == pos.shape and (t.stride(0) == 1 or t.shape[0] == 1)), where,
+                 f"{name} must be contiguous [tokens]")
+    return pos.shape[0]
+
+
+def pi_kv_append(a, cache, table, pos, q, k, v, q_out, seq=None, q_norm=None, k_norm=None, stream=None):
+    """q, q_out [tokens, heads, dim], k and v [tokens, kv heads, dim]; `pos` (and `seq`) int32 [tokens]."""
+    w = "pi_kv_append"
+    d = _handle_desc(a, "attention", w)
+    tokens = _places(w, d, pos, seq)
+    _on(d["device"], w, q=q, k=k, v=v, q_out=q_out, q_norm=q_norm, k_norm=k_norm)
+    _require(q.dtype == k.dtype == v.dtype == q_out.dtype, w, "q, k, v and q_out must have one type")
+    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+        _require(t is None or (str(t.dtype) == "torch.float32" and t.is_contiguous() and t.numel() == d["dim"]), w,
+                 f"{name} must be contiguous float32 [head_dim]")
+    strides = [_token_rows(t, w, name, tokens, n, d["dim"]) for name, t, n in
+               (("q", q, d["heads"]), ("k", k, d["kv_heads"]), ("v", v, d["kv_heads"]), ("q_out", q_out, d["heads"]))]
+    _check(lib().pi_kv_append(a, _cache_arg(cache, d, w), _table_arg(table, d, w), tokens, _ptr(seq), _ptr(pos),
+                              _float_code(q, w, "q"), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
+                              _ptr(q_norm), _ptr(k_norm), _ptr(q_out), strides[3], _stream_on(stream, d["device"])), w)
+
+
+def pi_kv_read(a, cache, table, pos, k_out, v_out, seq=None, stream=None):
+    """k_out and v_out: contiguous [tokens, kv heads, dim] of one type."""
+    w = "pi_kv_read"
+    d = _handle_desc(a, "attention", w)
+    tokens = _places(w, d, pos, seq)
+    _on(d["device"], w, k_out=k_out, v_out=v_out)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _require(tuple(t.shape) == (tokens, d["kv_heads"], d["dim"]) and t.is_contiguous() and t.dtype == k_out.dtype, w,
+                 f"{name} must be contiguous {[tokens, d['kv_heads'], d['dim']]}, both of one type")
+    _check(lib().pi_kv_read(a, _cache_arg(cache, d, w), _table_arg(table, d, w), tokens, _ptr(seq), _ptr(pos),
+                            _float_code(k_out, w, "k_out"), _ptr(k_out), _ptr(v_out), _stream_on(stream, d["device"])), w)
+
+
+def pi_paged_attention(a, cache, table, lens, q, out, lse=None, stream=None):
+    """q and out [sequences, heads, dim]; `lens` int32 [sequences]; `lse` float32 [sequences, heads] or None."""
+    w = "pi_paged_attention"
+    d = _handle_desc(a, "attention", w)
+    n = table.shape[0]
+    _int32(w, lens=lens)
+    _on(d["device"], w, lens=lens, q=q, out=out, lse=lse)
+    _require(tuple(lens.shape) == (n,) and (lens.stride(0) == 1 or n == 1), w, "lens must be contiguous [sequences]")
+    _require(q.dtype == out.dtype, w, "q and out must have one type")
+    qs, os_ = _token_rows(q, w, "q", n, d["heads"], d["dim"]), _token_rows(out, w, "out", n, d["heads"], d["dim"])
+    _require(lse is None or (tuple(lse.shape) == (n, d["heads"]) and str(lse.dtype) == "torch.float32"
+                             and lse.is_contiguous()), w, "lse must be contiguous float32 [sequences, heads]")
+    _check(lib().pi_paged_attention(a, _cache_arg(cache, d, w), _table_arg(table, d, w), _ptr(lens),
+                                    _float_code(q, w, "q"), _ptr(q), qs, _ptr(out), os_, _ptr(lse),
+                                    _stream_on(stream, d["device"])), w)

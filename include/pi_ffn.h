@@ -75,8 +75,8 @@ typedef enum { PI_ACT_RELU = 0, PI_ACT_REGLU = 1, PI_ACT_DRELU = 2 } pi_act;
 /* Stored formats.  INT4G32: symmetric 4-bit, value = s * (n - 8) with n the
  * nibble (low nibble = even element) and s one fp16 scale per 32 consecutive
  * elements of a neuron vector (a W_gate/W_up row or a W_down column).
- * I8 (predictor only): symmetric 8-bit, value = s * q with q a signed byte and
- * s one fp32 scale per row of U and of V -- the cheaper predictor (predictors
+ * I8 (predictor and key-value cache only): symmetric 8-bit, value = s * q with q a
+ * signed byte and s one fp32 scale per row of U and of V (of a cached vector) -- the cheaper predictor (predictors
  * are costly in memory: PowerInfer (unite.ai), "Adaptive sparse predictor"),
  * half the bytes of a 16-bit one. */
 typedef enum { PI_F32 = 0, PI_F16 = 1, PI_BF16 = 2, PI_INT4G32 = 3, PI_I8 = 4 } pi_dtype;
@@ -350,6 +350,153 @@ PI_API pi_status pi_predict_noalloc(int d_model, int d_ff, int rank, pi_dtype pr
                                     float threshold, const void *V_dev, const void *U_dev,
                                     const float *bias_dev, const float *x_dev, int32_t *idx_dev,
                                     int32_t *count_dev, float *z_dev, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The attention half of a decode layer
+ *
+ * The calls above run r <- r + FFN(RMSNorm(r)).  The calls below are the other
+ * half of a layer, on the same residual and in the same stored formats:
+ *   qkv = W_qkv RMSNorm(r)         pi_int4_matvec (norm_eps > 0)
+ *   q, k normed and rotated; k and v into the cache       pi_kv_append
+ *   o = attention of q over the cached positions          pi_paged_attention
+ *   r <- r + W_o o                 pi_int4_matvec (add_dev = y_dev = r)
+ * (the pages describe the FFN only; attention follows the usual definition
+ * written at each call).  Conventions as above.  Calls restore the current
+ * device before they return; each runs on its handle's device, which the
+ * stream has to belong to.  No call allocates device memory except the two
+ * create calls, so all others may be captured into CUDA graphs.
+ */
+
+/* One INT4G32 matrix W, n_rows x n_cols (n_cols a multiple of 32), for products
+ * with the activations of a few tokens.
+ *   q_dev  n_rows x n_cols/2 bytes of nibbles, 16-byte aligned; s_dev  n_rows x
+ *   n_cols/32 fp16 scales (format: see PI_INT4G32).
+ * Copied and laid out in library-owned memory (n_rows rounded up to 16 and
+ * n_cols to 64, times 9/16 bytes); the call synchronises `stream` before it
+ * returns, so the caller's buffers may be freed.  1 <= n_rows <= 2^20,
+ * 32 <= n_cols <= 2^17. */
+typedef struct pi_int4 *pi_int4_t;
+PI_API pi_status pi_int4_create(int n_rows, int n_cols, const void *q_dev, const void *s_dev, int device,
+                                void *stream, pi_int4_t *out);
+PI_API void pi_int4_destroy(pi_int4_t m);
+
+/* y_t = add_t + W f(x_t) for n_tokens tokens (1..32), f the identity or, with
+ * norm_eps > 0, f(x) = x / sqrt(mean(x^2) + norm_eps) (no weight: the norm of
+ * the decode calls).
+ *   x_dev    n_tokens rows of n_cols values [x_dtype], x_stride elements apart;
+ *            address and row distance multiples of 16 bytes
+ *   add_dev  NULL, or rows like y's (may be y_dev itself: y += W f(x))
+ *   y_dev    n_tokens rows of n_rows values [y_dtype], y_stride elements apart
+ * Types F32, F16 or BF16.  Products are exact (x in parts that hold all its
+ * bits), sums are fp32, y is rounded once.  Each token's row depends on that
+ * token alone, the result is deterministic, and calls on several streams may
+ * overlap.  x must not overlap y, nor add overlap y unless both are the same
+ * rows.  Errors: PI_ERR_INVALID_ARG, PI_ERR_CUDA. */
+PI_API pi_status pi_int4_matvec(pi_int4_t m, int n_tokens, pi_dtype x_dtype, const void *x_dev, int64_t x_stride,
+                                const void *add_dev, pi_dtype y_dtype, void *y_dev, int64_t y_stride,
+                                float norm_eps, void *stream);
+
+/* Heads, cache format and constants shared by an attention layer's calls (one
+ * handle serves all layers of the same shape). */
+typedef enum { PI_KV_HND = 0, PI_KV_NHD = 1 } pi_kv_layout;
+typedef struct {
+    int n_heads;           /* query heads, a multiple of n_kv_heads; <= 1024 */
+    int n_kv_heads;        /* query head h reads cached head h / (n_heads / n_kv_heads) */
+    int head_dim;          /* 64 or 128 */
+    pi_dtype cache_dtype;  /* F16, BF16, I8 or INT4G32 */
+    int page_size;         /* positions per page: a power of two, 8..256 */
+    pi_kv_layout layout;   /* rows of a page by head (HND) or by position (NHD) */
+    int rotary_dim;        /* leading elements of q and k that are rotated: even, <= head_dim; 0 = none */
+    int rotary_pairs;      /* 0: pairs (i, i + rotary_dim/2); 1: pairs (2i, 2i + 1) */
+    float rope_theta;      /* pair i turns by position * rope_theta^(-2i/rotary_dim); > 0 if rotated */
+    float norm_eps;        /* > 0: q and k heads are normed before the rotation; 0: not */
+    float scale;           /* score factor; 0 = 1 / sqrt(head_dim) */
+    float softcap;         /* > 0: score s becomes softcap * tanh(s / softcap); 0: not */
+    int window;            /* > 0: a position sees itself and the window - 1 positions before it; 0: all */
+    int device;
+} pi_attn_desc;
+
+typedef struct pi_attn *pi_attn_t;
+PI_API pi_status pi_attn_create(const pi_attn_desc *desc, pi_attn_t *out);
+PI_API void pi_attn_destroy(pi_attn_t a);
+
+/* Wait for `stream`, report (then clear) the handle's device error word:
+ * PI_ERR_DEVICE_CHECK after a call that met a sequence, a position, a length
+ * or a page out of range.  Such a token was skipped (pi_kv_append, pi_kv_read)
+ * or such positions left out of the softmax (pi_paged_attention); no memory
+ * out of range is touched. */
+PI_API pi_status pi_attn_sync(pi_attn_t a, void *stream);
+
+/* Caller-owned cache of one layer.  A row is one position of one head; row
+ * number ((page * n_kv_heads + head) * page_size + slot) for HND and
+ * ((page * page_size + slot) * n_kv_heads + head) for NHD, offsets in 64 bits.
+ *   F16 / BF16  k, v: rows of head_dim values; scales NULL
+ *   I8          rows of head_dim signed bytes; k_scale, v_scale: one fp32 each;
+ *               s = max|w| / 127, q = round_half_even(w / s) in [-127, 127]
+ *   INT4G32     rows of head_dim/2 bytes of nibbles; head_dim/32 fp16 scales
+ *               each; s = fp16(max|w| / 7), q = round_half_even(w / s) in [-8, 7]
+ * (a row or group of zeros, or one whose scale rounds to 0, has q = 0).  Values
+ * that are not finite, or too large for the scale's type, make their row's (I8)
+ * or group's (INT4G32) scale not finite: all of it then reads back as NaN.  All pointers 16-byte aligned. */
+typedef struct {
+    void *k, *v;
+    void *k_scale, *v_scale;
+    int n_pages;
+} pi_kv_cache;
+
+/* Page table: sequence s holds position p in page pages[s * stride + p / page_size]
+ * (device int32).  Entries behind the positions in use are not read. */
+typedef struct {
+    const int32_t *pages;
+    int n_seqs;
+    int width;             /* entries per sequence */
+    int64_t stride;        /* elements between sequences, >= width */
+} pi_kv_table;
+
+/* Queries and keys normed and rotated, keys and values written to the cache.
+ * Token t is position pos_dev[t] of sequence seq_dev[t] (seq_dev NULL: of
+ * sequence t); a negative position is an empty place: nothing of it is read or
+ * written.
+ *   q_dev, k_dev, v_dev  [dtype F32, F16 or BF16] token rows of n_heads, n_kv_heads
+ *            and n_kv_heads vectors of head_dim, *_stride elements apart
+ *            (address and row distance multiples of 16 bytes)
+ *   q_norm_dev, k_norm_dev  head_dim floats, or NULL for ones; NULL if norm_eps is 0
+ *   q_out_dev  as q_dev [dtype]; may be q_dev itself
+ *   x -> R_pos(w x / sqrt(mean(x^2) + norm_eps)), the rotation's angle in 64 bits.
+ * Keys are computed in 64 bits, so that the codes of a quantised cache do not
+ * hang on rounding; queries in 32.  Two tokens of a call must not be the same
+ * position of a sequence, and two sequences must not write the same page: what
+ * such rows then hold is unspecified.  At most 2^20 tokens. */
+PI_API pi_status pi_kv_append(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_table *table, int n_tokens,
+                              const int32_t *seq_dev, const int32_t *pos_dev, pi_dtype dtype,
+                              const void *q_dev, int64_t q_stride, const void *k_dev, int64_t k_stride,
+                              const void *v_dev, int64_t v_stride, const float *q_norm_dev,
+                              const float *k_norm_dev, void *q_out_dev, int64_t q_out_stride, void *stream);
+
+/* Rows of the cache as values: k_dev and v_dev [dtype], n_tokens x n_kv_heads x
+ * head_dim, 16-byte aligned, row t holding position pos_dev[t] of sequence
+ * seq_dev[t] (NULL: t); rows of negative positions are left as they were.
+ * Any row may be read any number of times. */
+PI_API pi_status pi_kv_read(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_table *table, int n_tokens,
+                            const int32_t *seq_dev, const int32_t *pos_dev, pi_dtype dtype, void *k_dev,
+                            void *v_dev, void *stream);
+
+/* Attention of one query per sequence over its first len_dev[s] positions (the
+ * query stands at position len - 1):
+ *   s_j = scale q . k_j (capped), j in [max(0, len - window), len)
+ *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ *   q_dev, out_dev  [dtype] rows of n_heads x head_dim, *_stride elements apart
+ *            (address and row distance multiples of 16 bytes); out must not
+ *            overlap q
+ *   lse_dev  NULL, or n_seqs x n_heads floats
+ * A sequence of length 0 gives out = 0 and lse = -infinity.  A negative length
+ * counts as 0, one above width * page_size as that (both are reported).
+ * Rows of the cache outside the window are not read.  The result is
+ * deterministic for given lengths.  Calls on one handle use its scratch and
+ * must not overlap; a captured graph's launches count as such calls. */
+PI_API pi_status pi_paged_attention(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_table *table,
+                                    const int32_t *len_dev, pi_dtype dtype, const void *q_dev, int64_t q_stride,
+                                    void *out_dev, int64_t out_stride, float *lse_dev, void *stream);
 
 #ifdef __cplusplus
 }
