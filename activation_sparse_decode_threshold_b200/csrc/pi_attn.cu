@@ -305,8 +305,8 @@ static pi_status cache_view(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_t
     if (cache->n_pages < 1) return fail(PI_ERR_INVALID_ARG, "n_pages must be >= 1");
     if (reinterpret_cast<uintptr_t>(table->pages) & 3u) return fail(PI_ERR_INVALID_ARG, "page table must be 4-byte aligned");
     if (table->n_seqs < 1 || table->n_seqs > 65536) return fail(PI_ERR_INVALID_ARG, "n_seqs must be in [1, 65536]");
-    if (table->width < 1 || (long long)table->width * D.page_size > 0x7fffffffLL)
-        return fail(PI_ERR_INVALID_ARG, "width must be >= 1 and width * page_size below 2^31");
+    if (table->width < 1 || (long long)table->width * D.page_size > (1LL << 30))
+        return fail(PI_ERR_INVALID_ARG, "width must be >= 1 and width * page_size at most 2^30");
     if (table->n_seqs > 1 && (table->stride < table->width || table->stride > kMaxStride))
         return fail(PI_ERR_INVALID_ARG, "page table: row distance below width (or above 2^40)");
     c.k = static_cast<uint8_t *>(cache->k);

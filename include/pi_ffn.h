@@ -445,11 +445,12 @@ typedef struct {
 } pi_kv_cache;
 
 /* Page table: sequence s holds position p in page pages[s * stride + p / page_size]
- * (device int32).  Entries behind the positions in use are not read. */
+ * (device int32).  Entries behind the positions in use are not read.  At most
+ * 65536 sequences. */
 typedef struct {
     const int32_t *pages;
     int n_seqs;
-    int width;             /* entries per sequence */
+    int width;             /* entries per sequence; width * page_size at most 2^30 */
     int64_t stride;        /* elements between sequences, >= width */
 } pi_kv_table;
 
