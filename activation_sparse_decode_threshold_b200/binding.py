@@ -273,54 +273,67 @@ def pi_predict_noalloc(d_model, d_ff, rank, pred_dtype, threshold, V, U, bias, x
 # ---------------------------------------------------------------------------
 KV_LAYOUT = {"hnd": 0, "nhd": 1}
 _desc: dict = {}     # handle -> what the checks need of it
+_types: dict = {}    # torch's types, once a tensor has been seen
+_raw_stream = None
 
 
-def _require(ok, where: str, msg: str):
-    if not ok:
-        raise PiError(PI_ERR_INVALID_ARG, where, msg)
+def _torch_types():
+    """torch is imported by the first call that is given a tensor, as everywhere in this file."""
+    global _raw_stream
+    if not _types:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _types.update(float={torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}, f32=torch.float32, f16=torch.float16,
+                      bf16=torch.bfloat16, i8=torch.int8, u8=torch.uint8, i32=torch.int32)
+    return _types
+
+
+def _bad(where: str, msg: str):
+    raise PiError(PI_ERR_INVALID_ARG, where, msg)
 
 
 def _float_code(t, where: str, name: str) -> int:
-    code = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}.get(str(t.dtype))
-    _require(code is not None, where, f"{name} must be float32, float16 or bfloat16")
+    code = _torch_types()["float"].get(t.dtype)
+    if code is None:
+        _bad(where, f"{name} must be float32, float16 or bfloat16")
     return code
 
 
-def _on(device: int, where: str, **tensors):
-    for name, t in tensors.items():
-        _require(t is None or (t.is_cuda and t.device.index == device), where, f"{name} is not on cuda:{device}")
-
-
-def _int32(where: str, **tensors):
-    for name, t in tensors.items():
-        _require(t is None or str(t.dtype) == "torch.int32", where, f"{name} must be int32")
+def _off_device(where: str, name: str, device: int):
+    _bad(where, f"{name} is not on cuda:{device}")
 
 
 def _stream_on(stream, device: int):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
-    return _stream(stream)
+        if _raw_stream is None:
+            _torch_types()
+        return _raw_stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _handle_desc(h, kind: str, where: str):
     d = _desc.get(h)
-    _require(d is not None and d["kind"] == kind, where, f"not a live {kind} handle")
+    if d is None or d["kind"] != kind:
+        _bad(where, f"not a live {kind} handle")
     return d
 
 
 def pi_int4_create(q, s, device=None, stream=None) -> int:
     """`q`: uint8 [n_rows x n_cols/2] nibbles, `s`: float16 [n_rows x n_cols/32], both contiguous on the device."""
-    w = "pi_int4_create"
-    _require(q.is_cuda and s.is_cuda, w, "q and s must be CUDA tensors")
-    device = q.device.index if device is None else device
-    _on(device, w, q=q, s=s)
-    _require(q.dim() == 2 and str(q.dtype) == "torch.uint8" and q.is_contiguous(), w, "q must be contiguous uint8 [n, k/2]")
+    w, ty = "pi_int4_create", _torch_types()
+    if not (q.is_cuda and s.is_cuda):
+        _bad(w, "q and s must be CUDA tensors")
+    device = q.get_device() if device is None else device
+    if q.get_device() != device or s.get_device() != device:
+        _off_device(w, "q or s", device)
+    if q.dim() != 2 or q.dtype != ty["u8"] or not q.is_contiguous():
+        _bad(w, "q must be contiguous uint8 [n, k/2]")
     n, k = q.shape[0], 2 * q.shape[1]
-    _require(str(s.dtype) == "torch.float16" and s.is_contiguous() and tuple(s.shape) == (n, k // 32) and k % 32 == 0, w,
-             "s must be contiguous float16 [n, k/32]")
+    if k % 32 or s.dtype != ty["f16"] or not s.is_contiguous() or s.shape != (n, k // 32):
+        _bad(w, "s must be contiguous float16 [n, k/32]")
     h = ctypes.c_void_p()
-    _check(lib().pi_int4_create(n, k, _ptr(q), _ptr(s), device, _stream_on(stream, device), ctypes.byref(h)), w)
+    _check(lib().pi_int4_create(n, k, q.data_ptr(), s.data_ptr(), device, _stream_on(stream, device), ctypes.byref(h)), w)
     _desc[h.value] = {"kind": "int4", "n": n, "k": k, "device": device}
     return h.value
 
@@ -330,28 +343,34 @@ def pi_int4_destroy(m: int):
         lib().pi_int4_destroy(m)
 
 
-def _token_rows(t, where: str, name: str, tokens: int, *shape):
-    """Row distance of a [tokens, ...] tensor whose rows are contiguous."""
-    _require(tuple(t.shape) == (tokens, *shape), where, f"{name} must be {[tokens, *shape]}, not {list(t.shape)}")
-    want = 1
-    for n, st in zip(reversed(shape), reversed(t.stride()[1:])):
-        _require(n == 1 or st == want, where, f"{name}: a token's values must be contiguous")
-        want *= n
-    return t.stride(0)
+def _token_rows(t, where: str, name: str, device: int, shape: tuple, inner: tuple) -> int:
+    """Row distance of a tensor on `device` of this shape, [tokens, ...], whose rows are contiguous (strides `inner`)."""
+    st = t.stride()
+    if t.shape != shape:
+        _bad(where, f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if st[1:] != inner and any(n != 1 and a != b for n, a, b in zip(shape[1:], st[1:], inner)):
+        _bad(where, f"{name}: a token's values must be contiguous")
+    if t.get_device() != device:
+        _off_device(where, name, device)
+    return st[0]
 
 
 def pi_int4_matvec(m, x, y, add=None, norm_eps=0.0, stream=None):
     """y [tokens x n_rows] = add + W f(x), x [tokens x n_cols]."""
     w = "pi_int4_matvec"
     d = _handle_desc(m, "int4", w)
-    _on(d["device"], w, x=x, y=y, add=add)
-    tokens = x.shape[0]
-    xs, ys = _token_rows(x, w, "x", tokens, d["k"]), _token_rows(y, w, "y", tokens, d["n"])
+    device, tokens = d["device"], x.shape[0]
+    xs = _token_rows(x, w, "x", device, (tokens, d["k"]), (1,))
+    ys = _token_rows(y, w, "y", device, (tokens, d["n"]), (1,))
+    xc, yc, ap = _float_code(x, w, "x"), _float_code(y, w, "y"), None
     if add is not None:
-        _require(add.dtype == y.dtype and (_token_rows(add, w, "add", tokens, d["n"]) == ys or tokens == 1), w,
-                 "add must have y's type and row distance")
-    _check(lib().pi_int4_matvec(m, tokens, _float_code(x, w, "x"), _ptr(x), xs, _ptr(add), _float_code(y, w, "y"),
-                                _ptr(y), ys, norm_eps, _stream_on(stream, d["device"])), w)
+        if add is not y and ((_token_rows(add, w, "add", device, (tokens, d["n"]), (1,)) != ys and tokens != 1)
+                             or add.dtype != y.dtype):
+            _bad(w, "add must have y's type and row distance")
+        ap = add.data_ptr()
+    st = lib().pi_int4_matvec(m, tokens, xc, x.data_ptr(), xs, ap, yc, y.data_ptr(), ys, norm_eps, _stream_on(stream, device))
+    if st:
+        _check(st, w)
 
 
 def pi_attn_create(n_heads, n_kv_heads, head_dim, cache_dtype="bf16", page_size=64, layout="hnd", rotary_dim=0,
@@ -359,14 +378,16 @@ def pi_attn_create(n_heads, n_kv_heads, head_dim, cache_dtype="bf16", page_size=
                    device=0) -> int:
     w = "pi_attn_create"
     code = {"i8": DTYPE["i8row"]}.get(cache_dtype, DTYPE.get(cache_dtype))
-    _require(code is not None, w, f"unknown cache_dtype {cache_dtype!r}")
-    _require(layout in KV_LAYOUT, w, f"unknown layout {layout!r}")
+    if code is None:
+        _bad(w, f"unknown cache_dtype {cache_dtype!r}")
+    if layout not in KV_LAYOUT:
+        _bad(w, f"unknown layout {layout!r}")
     desc = pi_attn_desc(n_heads, n_kv_heads, head_dim, code, page_size, KV_LAYOUT[layout], rotary_dim, int(rotary_pairs),
                         rope_theta, norm_eps, scale, softcap, window, device)
     h = ctypes.c_void_p()
     _check(lib().pi_attn_create(ctypes.byref(desc), ctypes.byref(h)), w)
     _desc[h.value] = {"kind": "attention", "heads": n_heads, "kv_heads": n_kv_heads, "dim": head_dim, "code": code,
-                      "page": page_size, "layout": layout, "device": device}
+                      "page": page_size, "layout": layout, "device": device, "inner": (head_dim, 1)}
     return h.value
 
 
@@ -388,89 +409,121 @@ class pi_kv_cache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.c = _kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
+        self.ref = ctypes.byref(self.c)
         self.checked = None
 
 
 def _cache_arg(cache, d, where):
     if cache.checked is not d:
-        row, dt, scale = {1: (d["dim"], "torch.float16", None), 2: (d["dim"], "torch.bfloat16", None),
-                          4: (d["dim"], "torch.int8", ((), "torch.float32")),
-                          3: (d["dim"] // 2, "torch.uint8", ((d["dim"] // 32,), "torch.float16"))}[d["code"]]
+        ty = _torch_types()
+        row, dt, scale = {1: (d["dim"], ty["f16"], None), 2: (d["dim"], ty["bf16"], None),
+                          4: (d["dim"], ty["i8"], ((), ty["f32"])),
+                          3: (d["dim"] // 2, ty["u8"], ((d["dim"] // 32,), ty["f16"]))}[d["code"]]
         lead = (cache.k.shape[0], d["kv_heads"], d["page"]) if d["layout"] == "hnd" else \
             (cache.k.shape[0], d["page"], d["kv_heads"])
         for name in ("k", "v"):
             t, s = getattr(cache, name), getattr(cache, name + "_scale")
-            _require(tuple(t.shape) == (*lead, row) and str(t.dtype) == dt and t.is_contiguous(), where,
-                     f"cache {name} must be contiguous {dt} {[*lead, row]}")
+            if t.shape != (*lead, row) or t.dtype != dt or not t.is_contiguous():
+                _bad(where, f"cache {name} must be contiguous {dt} {[*lead, row]}")
             if scale is None:
-                _require(s is None, where, f"a cache of {dt} has no scales")
-            else:
-                _require(s is not None and tuple(s.shape) == (*lead, *scale[0]) and str(s.dtype) == scale[1]
-                         and s.is_contiguous(), where, f"cache {name}_scale must be contiguous {scale[1]} {[*lead, *scale[0]]}")
-            _on(d["device"], where, **{name: t, name + "_scale": s})
+                if s is not None:
+                    _bad(where, f"a cache of {dt} has no scales")
+            elif s is None or s.shape != (*lead, *scale[0]) or s.dtype != scale[1] or not s.is_contiguous():
+                _bad(where, f"cache {name}_scale must be contiguous {scale[1]} {[*lead, *scale[0]]}")
+            if t.get_device() != d["device"] or (s is not None and s.get_device() != d["device"]):
+                _off_device(where, f"cache {name}", d["device"])
         cache.checked = d
-    return ctypes.byref(cache.c)
+    return cache.ref
 
 
 def _table_arg(table, d, where):
-    _int32(where, table=table)
-    _on(d["device"], where, table=table)
-    _require(table.dim() == 2 and (table.stride(1) == 1 or table.shape[1] == 1), where,
-             "table must be [sequences, pages] with contiguous rows")
-    return ctypes.byref(_kv_table(_ptr(table), table.shape[0], table.shape[1], table.stride(0)))
+    sh, st = table.shape, table.stride()
+    if table.dtype != _types["i32"]:
+        _bad(where, "table must be int32")
+    if len(sh) != 2 or (st[1] != 1 and sh[1] != 1):
+        _bad(where, "table must be [sequences, pages] with contiguous rows")
+    if table.get_device() != d["device"]:
+        _off_device(where, "table", d["device"])
+    return ctypes.byref(_kv_table(table.data_ptr(), sh[0], sh[1], st[0]))
 
 
-def _places(where, d, pos, seq):
-    _int32(where, pos=pos, seq=seq)
-    _on(d["device"], where, pos=pos, seq=seq)
-    for name, t in (("pos", pos), ("seq", seq)):
-        _require(t is None or (t.dim() == 1 and t.shape == pos.shape and (t.stride(0) == 1 or t.shape[0] == 1)), where,
-                 f"{name} must be contiguous [tokens]")
-    return pos.shape[0]
+def _ints(t, where, d, name, shape):
+    """Address of an int32 vector of this shape."""
+    if t.dtype != _torch_types()["i32"]:
+        _bad(where, f"{name} must be int32")
+    if t.shape != shape or len(shape) != 1 or (t.stride(0) != 1 and shape[0] != 1):
+        _bad(where, f"{name} must be contiguous {list(shape)}")
+    if t.get_device() != d["device"]:
+        _off_device(where, name, d["device"])
+    return t.data_ptr()
+
+
+def _norm_weight(t, where, d, name):
+    if t.dtype != _types["f32"] or not t.is_contiguous() or t.numel() != d["dim"]:
+        _bad(where, f"{name} must be contiguous float32 [head_dim]")
+    if t.get_device() != d["device"]:
+        _off_device(where, name, d["device"])
+    return t.data_ptr()
 
 
 def pi_kv_append(a, cache, table, pos, q, k, v, q_out, seq=None, q_norm=None, k_norm=None, stream=None):
     """q, q_out [tokens, heads, dim], k and v [tokens, kv heads, dim]; `pos` (and `seq`) int32 [tokens]."""
     w = "pi_kv_append"
     d = _handle_desc(a, "attention", w)
-    tokens = _places(w, d, pos, seq)
-    _on(d["device"], w, q=q, k=k, v=v, q_out=q_out, q_norm=q_norm, k_norm=k_norm)
-    _require(q.dtype == k.dtype == v.dtype == q_out.dtype, w, "q, k, v and q_out must have one type")
-    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
-        _require(t is None or (str(t.dtype) == "torch.float32" and t.is_contiguous() and t.numel() == d["dim"]), w,
-                 f"{name} must be contiguous float32 [head_dim]")
-    strides = [_token_rows(t, w, name, tokens, n, d["dim"]) for name, t, n in
-               (("q", q, d["heads"]), ("k", k, d["kv_heads"]), ("v", v, d["kv_heads"]), ("q_out", q_out, d["heads"]))]
-    _check(lib().pi_kv_append(a, _cache_arg(cache, d, w), _table_arg(table, d, w), tokens, _ptr(seq), _ptr(pos),
-                              _float_code(q, w, "q"), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
-                              _ptr(q_norm), _ptr(k_norm), _ptr(q_out), strides[3], _stream_on(stream, d["device"])), w)
+    device, dim, inner = d["device"], d["dim"], d["inner"]
+    pp = _ints(pos, w, d, "pos", pos.shape)
+    sp = None if seq is None else _ints(seq, w, d, "seq", pos.shape)
+    tokens = pos.shape[0]
+    qsh, ksh, code = (tokens, d["heads"], dim), (tokens, d["kv_heads"], dim), _float_code(q, w, "q")
+    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+        _bad(w, "q, k, v and q_out must have one type")
+    st = lib().pi_kv_append(
+        a, _cache_arg(cache, d, w), _table_arg(table, d, w), tokens, sp, pp, code,
+        q.data_ptr(), _token_rows(q, w, "q", device, qsh, inner), k.data_ptr(), _token_rows(k, w, "k", device, ksh, inner),
+        v.data_ptr(), _token_rows(v, w, "v", device, ksh, inner),
+        None if q_norm is None else _norm_weight(q_norm, w, d, "q_norm"),
+        None if k_norm is None else _norm_weight(k_norm, w, d, "k_norm"),
+        q_out.data_ptr(), _token_rows(q_out, w, "q_out", device, qsh, inner), _stream_on(stream, device))
+    if st:
+        _check(st, w)
 
 
 def pi_kv_read(a, cache, table, pos, k_out, v_out, seq=None, stream=None):
     """k_out and v_out: contiguous [tokens, kv heads, dim] of one type."""
     w = "pi_kv_read"
     d = _handle_desc(a, "attention", w)
-    tokens = _places(w, d, pos, seq)
-    _on(d["device"], w, k_out=k_out, v_out=v_out)
+    device = d["device"]
+    pp = _ints(pos, w, d, "pos", pos.shape)
+    sp = None if seq is None else _ints(seq, w, d, "seq", pos.shape)
+    shape = (pos.shape[0], d["kv_heads"], d["dim"])
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _require(tuple(t.shape) == (tokens, d["kv_heads"], d["dim"]) and t.is_contiguous() and t.dtype == k_out.dtype, w,
-                 f"{name} must be contiguous {[tokens, d['kv_heads'], d['dim']]}, both of one type")
-    _check(lib().pi_kv_read(a, _cache_arg(cache, d, w), _table_arg(table, d, w), tokens, _ptr(seq), _ptr(pos),
-                            _float_code(k_out, w, "k_out"), _ptr(k_out), _ptr(v_out), _stream_on(stream, d["device"])), w)
+        if t.shape != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
+            _bad(w, f"{name} must be contiguous {list(shape)}, both of one type")
+        if t.get_device() != device:
+            _off_device(w, name, device)
+    st = lib().pi_kv_read(a, _cache_arg(cache, d, w), _table_arg(table, d, w), shape[0], sp, pp, _float_code(k_out, w, "k_out"),
+                          k_out.data_ptr(), v_out.data_ptr(), _stream_on(stream, device))
+    if st:
+        _check(st, w)
 
 
 def pi_paged_attention(a, cache, table, lens, q, out, lse=None, stream=None):
     """q and out [sequences, heads, dim]; `lens` int32 [sequences]; `lse` float32 [sequences, heads] or None."""
     w = "pi_paged_attention"
     d = _handle_desc(a, "attention", w)
-    n = table.shape[0]
-    _int32(w, lens=lens)
-    _on(d["device"], w, lens=lens, q=q, out=out, lse=lse)
-    _require(tuple(lens.shape) == (n,) and (lens.stride(0) == 1 or n == 1), w, "lens must be contiguous [sequences]")
-    _require(q.dtype == out.dtype, w, "q and out must have one type")
-    qs, os_ = _token_rows(q, w, "q", n, d["heads"], d["dim"]), _token_rows(out, w, "out", n, d["heads"], d["dim"])
-    _require(lse is None or (tuple(lse.shape) == (n, d["heads"]) and str(lse.dtype) == "torch.float32"
-                             and lse.is_contiguous()), w, "lse must be contiguous float32 [sequences, heads]")
-    _check(lib().pi_paged_attention(a, _cache_arg(cache, d, w), _table_arg(table, d, w), _ptr(lens),
-                                    _float_code(q, w, "q"), _ptr(q), qs, _ptr(out), os_, _ptr(lse),
-                                    _stream_on(stream, d["device"])), w)
+    device, inner, n = d["device"], d["inner"], table.shape[0]
+    lp, code, shape = _ints(lens, w, d, "lens", (n,)), _float_code(q, w, "q"), (n, d["heads"], d["dim"])
+    if q.dtype != out.dtype:
+        _bad(w, "q and out must have one type")
+    qs, os_ = _token_rows(q, w, "q", device, shape, inner), _token_rows(out, w, "out", device, shape, inner)
+    ep = None
+    if lse is not None:
+        if lse.shape != shape[:2] or lse.dtype != _types["f32"] or not lse.is_contiguous():
+            _bad(w, "lse must be contiguous float32 [sequences, heads]")
+        if lse.get_device() != device:
+            _off_device(w, "lse", device)
+        ep = lse.data_ptr()
+    st = lib().pi_paged_attention(a, _cache_arg(cache, d, w), _table_arg(table, d, w), lp, code, q.data_ptr(), qs,
+                                  out.data_ptr(), os_, ep, _stream_on(stream, device))
+    if st:
+        _check(st, w)
