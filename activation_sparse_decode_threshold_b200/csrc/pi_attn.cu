@@ -249,7 +249,7 @@ pi_status pi_attn_create(const pi_attn_desc *desc, pi_attn_t *out)
     for (int i = 0; i < D.rotary_dim / 2; ++i) freq[i] = std::pow(double(D.rope_theta), -2.0 * i / D.rotary_dim);
     const size_t o_err = sizeof freq, o_tick = o_err + 256;
     const size_t o_part = (o_tick + pi::attn_ticket_bytes(n_sm) + 255) & ~size_t(255);
-    const size_t total = o_part + pi::attn_part_bytes(n_sm);
+    const size_t total = o_part + pi::attn_part_bytes(n_sm, D.n_heads / D.n_kv_heads);
     cudaError_t e = pi::attn_setup();
     if (e == cudaSuccess) e = cudaMalloc(&a->scratch, total);
     if (e == cudaSuccess) e = cudaMemset(a->scratch, 0, total);

@@ -81,7 +81,7 @@ struct AttnParams {
     int *err;
     int n_sm;
 };
-size_t attn_part_bytes(int n_sm);
+size_t attn_part_bytes(int n_sm, int group);
 size_t attn_ticket_bytes(int n_sm);
 cudaError_t attn_setup();   // once per device, before any launch
 cudaError_t paged_attention(const AttnParams &p, cudaStream_t st);

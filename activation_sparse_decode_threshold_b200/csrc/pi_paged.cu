@@ -9,13 +9,17 @@
 // the work, all sequences' chunks of 16 positions for each cached head, is laid
 // end to end and shared out evenly over all warps, whatever the lengths; a warp
 // keeps its chunks coming by asynchronous copies several chunks ahead.  Products
-// run on mma.sync m16n8k16, 8 query heads at a time as rows 0-7; rows 8-15 carry
-// the low parts of the same 8 heads (queries and weights as two 16-bit parts,
-// products with the 16-bit, 8-bit or 4-bit codes exact), which costs nothing:
-// the rows would be empty.  Scales of quantised rows are applied in fp32 to the
-// scores (K) and to the weights (V).
+// run on mma.sync m16n8k16 with the cache as the matrix of 16 rows (positions
+// for the scores, elements of V for the sums) and 4 query heads as 8 columns:
+// column 2h holds head h's queries or weights in 16 bits, column 2h + 1 what
+// that rounding left, so that the products are those of 22 (bf16: 16) bits with
+// the cache's 16-, 8- or 4-bit numbers, which are exact.  A head's two columns
+// meet in one lane.  Scales of quantised rows are applied in fp32, to the scores
+// (K) and to the weights (V).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "pi_attn.h"
 
@@ -23,27 +27,40 @@ namespace pi {
 namespace {
 
 constexpr int kChunk = 16;            // positions
-constexpr int kMaxWarps = 12;
-constexpr int kHeads = 8;             // query heads of an item
 
-template <int FMT, int D>
+// FMT: the cache's format.  NB: tiles of 4 query heads that share a cached head.
+template <int FMT, int D, int NB>
 struct Cfg {
     static constexpr bool kF = FMT == kF16 || FMT == kBF16;
     static constexpr int kRow = FMT == kI8 ? D : FMT == kI4 ? D / 2 : 2 * D;   // bytes of a cached row
     static constexpr int kScale = FMT == kI8 ? 4 : FMT == kI4 ? D / 16 : 0;    // bytes of its scales
+    static constexpr int kPieces = kRow / 16;
     static constexpr int kCodes = kChunk * kRow;                              // bytes of a chunk's K (or V)
     static constexpr int kOffV = kCodes, kOffS = 2 * kCodes, kOffI = kOffS + (kScale ? 256 : 0);
     static constexpr int kStage = kOffI + 16;
-    static constexpr int kWarps = 8;
-    static constexpr int kStages = FMT == kI4 ? 8 : FMT == kI8 ? 6 : 3;
+    static constexpr int kHeads = 4 * NB;                                     // query heads of an item
+    static constexpr int kStep = D / 16;                                      // products of 16 along the head
+    static constexpr bool kQShared = NB * D >= 512;                           // queries in shared memory, not registers
+    static constexpr int kQ = kQShared ? kStep * NB * 256 : 0;
+    // Warps of a CTA: 16 where 128 registers do; 16-bit rows of 256 bytes leave room for three stages of 8 warps.
+    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : 8) : NB * D <= 128 ? 16 : 8;
+    static constexpr int kDP = D + 8;                                         // a head's distance in a partial result
+    static constexpr int kPart = kHeads * (kDP + 2) * 4;                      // its bytes: o, then m and l
+    static constexpr int kRoom = 220 * 1024 / kWarps;
+    static constexpr int kStages = (kRoom - kQ) / kStage < 8 ? (kRoom - kQ) / kStage : 8;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kPart = kHeads * D * 4 + 2 * kHeads * 4;             // bytes of a partial result
-    static constexpr int kSmem = kWarps * kRing;
-    static_assert(kRing >= kPart, "a warp's partial result takes the place of its ring");
-    static_assert(kSmem <= 227 * 1024, "");
+    static constexpr int kSmem = kWarps * (kRing + kQ);
+    static_assert(kStages >= 3 && kRing >= kPart && kPart % 16 == 0 && kRing % 16 == 0 && kSmem + 8448 <= 227 * 1024, "");
 };
 
 __device__ __forceinline__ uint32_t s2u(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ float exp2_(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Copies of 16, 8 or 4 bytes; `live` false writes zeros and reads nothing.
 template <int N>
@@ -57,12 +74,6 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a)
 {
     uint2 v;
@@ -75,50 +86,54 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a)
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-
-__device__ __forceinline__ float exp2_(float x)
+// Four 8x8 matrices of 16-bit units, rows at the addresses of lanes 0-7, 8-15, ...
+template <bool TRANS>
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4])
 {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 template <bool BF>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint2 b)
 {
     if (BF)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                      "{%8, %9}, {%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
     else
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                      "{%8, %9}, {%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
-// Two numbers as 16-bit high parts and what is left of them as low parts.
+// A number as its 16-bit rounding (low half) and the rounding of what is left (high half).
 template <bool BF>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ uint32_t split(float v)
 {
     if (BF) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(a - f.x, b - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
+        const __nv_bfloat16 h = __float2bfloat16(v);
+        const __nv_bfloat162 p = __halves2bfloat162(h, __float2bfloat16(v - __bfloat162float(h)));
+        return *reinterpret_cast<const uint32_t *>(&p);
     }
+    const __half h = __float2half(v);
+    const __half2 p = __halves2half2(h, __float2half(v - __half2float(h)));
+    return *reinterpret_cast<const uint32_t *>(&p);
 }
-
-// A sum's high and low part as one number.  An infinite high part stands alone:
-// its low part holds 0 times that infinity.
+// The two parts' sum.  An infinite high part stands alone: its low part holds 0
+// times that infinity.
 __device__ __forceinline__ float whole(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
 
 __device__ __forceinline__ uint32_t hsub(uint32_t v, uint32_t m)
@@ -126,54 +141,37 @@ __device__ __forceinline__ uint32_t hsub(uint32_t v, uint32_t m)
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&m));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
-// Eight 4-bit codes n to four fp16 pairs n - 8: nibbles (i, i + 4) to pair i.
-__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&r)[4])
+__device__ __forceinline__ uint32_t hfma(uint32_t v, uint32_t a, uint32_t b)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = hsub(((w >> (4 * i)) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+    const __half2 d = __hfma2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&a),
+                              *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
-// Bytes (0, 1) and (2, 3) of w, signed bytes with the top bit flipped, to fp16 pairs.
-__device__ __forceinline__ uint32_t bytes01(uint32_t w) { return hsub(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u); }
-__device__ __forceinline__ uint32_t bytes23(uint32_t w) { return hsub(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u); }
+// Two bytes of w (signed, with the top bit flipped) as an fp16 pair: under the
+// exponent of 1024 a byte b is 1024 + b.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t bytes(uint32_t w) { return hsub(__byte_perm(w, 0x64646464u, SEL), 0x64806480u); }
 
-// Eight consecutive inputs as floats.
-__device__ __forceinline__ void load8(const uint8_t *p, long long i, int dt, float (&v)[8])
+// Two numbers' 16-bit roundings, or (low) the roundings of what is left.
+template <bool BF>
+__device__ __forceinline__ uint32_t part_pair(float a, float b, bool low)
 {
-    if (dt == kF32) {
-        const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-        const float4 a = q[0], b = q[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p + 2 * i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = dt == kF16 ? __half22float2(*reinterpret_cast<const __half2 *>(&u[e]))
-                                        : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e]));
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-        }
+    if (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(a - f.x, b - f.y);
+        return low ? *reinterpret_cast<const uint32_t *>(&l) : *reinterpret_cast<const uint32_t *>(&h);
     }
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    return low ? *reinterpret_cast<const uint32_t *>(&l) : *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b, int dt)
+__device__ __forceinline__ void output(uint8_t *p, long long i, int dt, float v)
 {
-    if (dt == kF16) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ void store8(uint8_t *p, long long i, int dt, const float (&v)[8])
-{
-    if (dt == kF32) {
-        float4 *q = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(pack2(v[0], v[1], dt), pack2(v[2], v[3], dt),
-                                                           pack2(v[4], v[5], dt), pack2(v[6], v[7], dt));
-    }
+    if (dt == kF32) reinterpret_cast<float *>(p)[i] = v;
+    else if (dt == kF16) reinterpret_cast<__half *>(p)[i] = __float2half(v);
+    else reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v);
 }
 
 // Positions of one sequence that its query sees, and the chunks that hold them.
@@ -183,8 +181,8 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const AttnParams &p, int s, bool report)
 {
-    int len = p.len[s];
-    const int room = p.c.width << p.c.page_shift;
+    int len = __ldg(p.len + s);
+    const int room = p.c.width << p.c.page_shift;   // at most 2^30
     if (len < 0 || len > room) {
         if (report) atomicExch(p.err, int(kDevCheck));
         len = len < 0 ? 0 : room;
@@ -197,11 +195,37 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int s, bool report)
     return r;
 }
 
+// A quotient of numbers >= 0: 32-bit arithmetic where it will do (a 64-bit division takes some 100 cycles more).
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return (a | b) >> 31 ? a / b : (long long)(unsigned(a) / unsigned(b));
+}
+
+// The work of a call in units: one for each chunk, and one before each item, for
+// its start (queries, the result).  Warp `share` of `shares` takes the units from
+// first(share) up to first(share + 1).
+struct Shares {
+    long long each, more;   // units of every share, shares that have one more
+    __device__ Shares(long long total, int shares) : each(quotient(total, shares)), more(total - each * shares) {}
+    __device__ long long first(long long share) const { return share * each + min(share, more); }
+    __device__ int of(long long unit) const
+    {
+        const long long big = more * (each + 1);
+        return int(unit < big ? quotient(unit, each + 1) : more + quotient(unit - big, each));   // (each > 0 if unit >= big)
+    }
+};
+
 // Where a warp is in the row of all chunks: sequence s, item i of the
-// sequence (cached head and block of 8 query heads), chunk c.
+// sequence (cached head and block of its query heads), chunk c.
 struct Cursor {
     int s, item, c;
     Span span;
+};
+
+// An item that has partial results in a CTA: their slots by bit, and the CTAs that hold its first and last chunk.
+struct Joint {
+    int s, item, a, b;
+    unsigned slots;
 };
 
 enum { kFirst = 1, kLast = 2, kWhole = 4 };   // a chunk in its segment; a segment that is its whole item
@@ -211,29 +235,32 @@ enum { kFirst = 1, kLast = 2, kWhole = 4 };   // a chunk in its segment; a segme
 // ref + 13) finite, for rows of zeros (s = 0).
 constexpr int kLeastRef = 16;
 
-// Scale factor of scores and accumulators by power of two, from a number's exponent.
+// A power of two from its exponent.
 __device__ __forceinline__ float pow2_of(int biased) { return __int_as_float(biased << 23); }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(32 * Cfg<FMT, D>::kWarps, 1) k_paged(AttnParams p, int items, int blocks_per_head)
+template <int FMT, int D, int NB>
+__global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnParams p, int items, int blocks_per_head)
 {
-    using C = Cfg<FMT, D>;
+    using C = Cfg<FMT, D, NB>;
     constexpr bool BF = FMT == kBF16;
-    constexpr int W = C::kWarps, S = C::kStages, NT = D / 8;
+    constexpr int W = C::kWarps, S = C::kStages, T = 32 * W, KS = C::kStep, P = C::kPieces, DP = C::kDP;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sums[W];
-    __shared__ long long offs[32 * W];
-    __shared__ int part_s[W][2], part_item[W][2];
-    __shared__ int is_last;
+    __shared__ long long offs[T];
+    // partial results: slot 2 w of warp w's first segment (in global memory), 2 w + 1 of its last (in its ring)
+    __shared__ int part_s[2 * W], part_item[2 * W];
+    __shared__ float part_m[2 * W][C::kHeads], part_l[2 * W][C::kHeads], part_f[2 * W][C::kHeads];
+    __shared__ Joint joints[2 * W];
+    __shared__ int n_joints, last[2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int n = p.c.n_seqs;
 
-    // ---- chunks before each thread's block of sequences --------------------
-    const int per = (n + 32 * W - 1) / (32 * W);
+    // ---- units before each thread's block of sequences --------------------
+    const int per = (n + T - 1) / T;
     long long mine = 0;
     for (int s = threadIdx.x * per; s < min(n, (int(threadIdx.x) + 1) * per); ++s) {
         const Span r = span_of(p, s, blockIdx.x == 0);
-        mine += (long long)(r.c1 - r.c0) * items;
+        mine += (long long)(r.c1 - r.c0 + 1) * items;
     }
     long long scan = mine;
 #pragma unroll
@@ -249,110 +276,98 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D>::kWarps, 1) k_paged(AttnParam
         before += w < warp ? sums[w] : 0;
         total += sums[w];
     }
-    offs[threadIdx.x] = before + scan - mine;
+    offs[threadIdx.x] = before + scan - mine;   // (blocks without sequences: the total)
     __syncthreads();
 
     // ---- this warp's share ---------------------------------------------------
     const long long want = (total + W - 1) / W;
-    const int ctas = int(want < gridDim.x ? want : gridDim.x);   // at least a chunk for each warp
+    const int ctas = int(want < gridDim.x ? want : gridDim.x);   // at least a unit for each warp
     if (int(blockIdx.x) >= ctas) return;
-    const long long shares = (long long)ctas * W, share = (long long)blockIdx.x * W + warp;
-    const long long u0 = total * share / shares, u1 = total * (share + 1) / shares;
-    const long long cta0 = total * blockIdx.x / ctas, cta1 = total * (blockIdx.x + 1LL) / ctas;
+    const Shares shares(total, ctas * W);
+    const long long u0 = shares.first(blockIdx.x * W + warp);
+    int left = int(shares.first(blockIdx.x * W + warp + 1) - u0);   // units not yet taken
     uint8_t *ring = smem + warp * C::kRing;
     const uint32_t ring_u = s2u(ring);
-    if (lane < 2) part_s[warp][lane] = -1;
+    uint2 *q_shared = reinterpret_cast<uint2 *>(smem + W * C::kRing + warp * C::kQ);
+    if (lane < 2) part_s[2 * warp + lane] = -1;
 
     Cursor at{};
-    if (u0 < u1) {
-        int b = 0;   // the block that holds chunk u0: the last one that starts at or before it
-        for (int step = 16 * W; step; step >>= 1)
-            if (b + step < 32 * W && offs[b + step] <= u0) b += step;
-        // (blocks without sequences start at the total, above u0)
+    if (left > 0) {
+        int b = 0, end = T;   // the block that holds unit u0: the last one that starts at or before it
+        while (end - b > 1) {
+            const int mid = (b + end) / 2;
+            if (offs[mid] <= u0) b = mid;
+            else end = mid;
+        }
         at.s = b * per;
-        long long left = u0 - offs[b];
+        long long rest = u0 - offs[b];
         for (;;) {
             at.span = span_of(p, at.s, false);
-            const long long here = (long long)(at.span.c1 - at.span.c0) * items;
-            if (left < here) break;
-            left -= here;
+            const long long here = (long long)(at.span.c1 - at.span.c0 + 1) * items;
+            if (rest < here) break;
+            rest -= here;
             ++at.s;
         }
-        const int nc = at.span.c1 - at.span.c0;
-        at.item = int(left / nc);
-        at.c = at.span.c0 + int(left - (long long)at.item * nc);
+        const int nu = at.span.c1 - at.span.c0 + 1;
+        at.item = int(quotient(rest, nu));
+        const int unit = int(rest - (long long)at.item * nu);   // 0: the item's start
+        if (unit == 0) --left;
+        at.c = at.span.c0 + max(unit - 1, 0);
     }
 
     // ---- copies of one chunk into a stage --------------------------------------
+    // Row r's 16-byte piece i lies at piece place(r, i): 8 rows' same pieces meet all banks once.
+    auto place = [](int r, int i) { return r * P + (i ^ (P >= 8 ? r & 7 : P == 4 ? (r >> 1) & 3 : (r >> 2) & 1)); };
+    constexpr int RI = 32 / P;            // rows of one copy instruction
+    const int my_row = lane / P, my_piece = lane % P;
     const long long slot_bytes = (long long)p.c.slot_rows * C::kRow, scale_slot = (long long)p.c.slot_rows * C::kScale;
-    int page_a = -1, page_b = -1;
-    auto look_up = [&]() {   // pages of the cursor's two halves of 8 positions
-        const int a = at.c * kChunk, b = a + 8;
-        const int32_t *row = p.c.table + at.s * p.c.tstride;
-        page_a = a < at.span.hi && a + 8 > at.span.lo ? row[a >> p.c.page_shift] : -1;
-        page_b = b < at.span.hi && b + 8 > at.span.lo ? row[b >> p.c.page_shift] : -1;
-    };
-    long long issued = u0;
-    bool first = true, from_start = u0 < u1 && at.c == at.span.c0;
-    if (u0 < u1) look_up();
+    // Pages of both halves of chunk page_c + lane of sequence page_s.
+    int page_s = -1, page_c = 0, page_a = -1, page_b = -1;
+    int issued = 0;
+    bool first = true, from_start = at.c == at.span.c0;
     auto issue = [&](int stage) {
-        if (issued >= u1) {
+        if (left <= 0) {
             copy_commit();
             return;
         }
+        if (at.s != page_s || unsigned(at.c - page_c) >= 32u) {
+            page_s = at.s;
+            page_c = at.c;
+            const int a = (at.c + lane) * kChunk, b = a + 8;   // (below 2^30 + 2^10)
+            const int32_t *row = p.c.table + at.s * p.c.tstride;
+            page_a = a < at.span.hi && a + 8 > at.span.lo ? __ldg(row + (a >> p.c.page_shift)) : -1;
+            page_b = b < at.span.hi && b + 8 > at.span.lo ? __ldg(row + (b >> p.c.page_shift)) : -1;
+        }
+        const int pa = __shfl_sync(~0u, page_a, at.c - page_c), pb = __shfl_sync(~0u, page_b, at.c - page_c);
         const int pos = at.c * kChunk;
         // positions seen, by bit
         unsigned mask = 0xffffu;
         if (pos + kChunk > at.span.hi) mask &= at.span.hi > pos ? (1u << (at.span.hi - pos)) - 1 : 0;
         if (pos < at.span.lo) mask &= ~((1u << (at.span.lo - pos)) - 1);
-        if ((mask & 0x00ffu) && (unsigned)page_a >= (unsigned)p.c.n_pages) {
+        if ((mask & 0x00ffu) && (unsigned)pa >= (unsigned)p.c.n_pages) {
             if (lane == 0) atomicExch(p.err, int(kDevCheck));
             mask &= 0xff00u;
         }
-        if ((mask & 0xff00u) && (unsigned)page_b >= (unsigned)p.c.n_pages) {
+        if ((mask & 0xff00u) && (unsigned)pb >= (unsigned)p.c.n_pages) {
             if (lane == 0) atomicExch(p.err, int(kDevCheck));
             mask &= 0x00ffu;
         }
-        const int hk = at.item / blocks_per_head;
-        const long long head = (long long)hk * p.c.head_rows;
         const int sm = p.c.page_size - 1;
-        const long long ra = (mask & 0x00ffu) ? (long long)page_a * p.c.page_rows + (long long)(pos & sm) * p.c.slot_rows + head : 0;
-        const long long rb = (mask & 0xff00u) ? (long long)page_b * p.c.page_rows + (long long)((pos + 8) & sm) * p.c.slot_rows + head : 0;
+        const long long head = (long long)(at.item / blocks_per_head) * p.c.head_rows;
+        const long long ra = (mask & 0x00ffu) ? (long long)pa * p.c.page_rows + (long long)(pos & sm) * p.c.slot_rows + head : 0;
+        const long long rb = (mask & 0xff00u) ? (long long)pb * p.c.page_rows + (long long)((pos + 8) & sm) * p.c.slot_rows + head : 0;
         const uint32_t dst = ring_u + stage * C::kStage;
         // a row without a position is filled with zeros (its memory is not read)
-        auto from = [&](const uint8_t *base, int key) {
-            return base + (key < 8 ? ra : rb) * C::kRow + ((mask >> key) & 1 ? (key & 7) * slot_bytes : 0);
-        };
-        if (C::kF || FMT == kI8) {
-            constexpr int JK = C::kRow / 64;   // 16-byte pieces of a K row for each lane of four
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < JK; ++j)
-                    copy_async<16>(dst + (h * JK + j) * 512 + lane * 16, from(p.c.k, g + 8 * h) + 16 * (t + 4 * j),
-                                   (mask >> (g + 8 * h)) & 1);
-            constexpr int JV = C::kRow >= 128 ? C::kRow / 128 : 1, NV = C::kRow >= 128 ? 16 : 8;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int key = 2 * t + (r & 1) + 8 * (r >> 1);
-#pragma unroll
-                for (int j = 0; j < JV; ++j)
-                    copy_async<NV>(dst + C::kOffV + (r * JV + j) * 32 * NV + lane * NV,
-                                   from(p.c.v, key) + NV * (g + 8 * j), (mask >> key) & 1);
-            }
-        } else {
-            // rows whole, their 16-byte pieces permuted so that later reads of one piece of 8 rows meet no bank twice
-            constexpr int P = C::kRow / 16;    // 4 or 2 pieces
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) {
-                const int key = P == 4 ? g + 8 * i : lane / 2, piece = P == 4 ? t : lane % 2;
-                const int put = key * C::kRow + 16 * (piece ^ ((key >> (P == 4 ? 1 : 2)) & (P - 1)));
-                const bool live = (mask >> key) & 1;
-                copy_async<16>(dst + put, from(p.c.k, key) + 16 * piece, live);
-                copy_async<16>(dst + C::kOffV + put, from(p.c.v, key) + 16 * piece, live);
-            }
+        for (int i = 0; i < kChunk / RI; ++i) {
+            const int row = my_row + i * RI;
+            const bool live = (mask >> row) & 1;
+            const long long off = (row < 8 ? ra : rb) * C::kRow + (live ? (row & 7) * slot_bytes : 0) + 16 * my_piece;
+            const uint32_t to = dst + 16 * place(row, my_piece);
+            copy_async<16>(to, p.c.k + off, live);
+            copy_async<16>(to + C::kOffV, p.c.v + off, live);
         }
-        if (C::kScale) {   // lanes 0-15: K of key lane, 16-31: V
+        if (C::kScale) {   // lanes 0-15: K of position lane, 16-31: V
             const int key = lane & 15;
             const bool live = (mask >> key) & 1;
             const uint8_t *base = (lane < 16 ? p.c.ks : p.c.vs) + (key < 8 ? ra : rb) * C::kScale +
@@ -361,63 +376,75 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D>::kWarps, 1) k_paged(AttnParam
         }
         copy_commit();
         // what the reader has to know
-        const bool ends = at.c + 1 == at.span.c1, last = ends || issued + 1 == u1;
+        const bool ends = at.c + 1 == at.span.c1, last = ends || left == 1;
         if (lane == 0)
             *reinterpret_cast<int4 *>(ring + stage * C::kStage + C::kOffI) =
                 make_int4(int(mask), (first ? kFirst : 0) | (last ? kLast : 0) | (ends && from_start ? kWhole : 0), at.s, at.item);
         first = last;
         ++issued;
-        if (!ends) ++at.c;
-        else if (issued < u1) {
-            if (++at.item == items) {
-                at.item = 0;
-                ++at.s;
-                at.span = span_of(p, at.s, false);
-            }
-            at.c = at.span.c0;
+        --left;
+        if (!ends) {
+            ++at.c;
+            return;
         }
-        if (last) from_start = true;
-        if (issued < u1) look_up();
+        from_start = true;
+        if (--left <= 0) return;   // (the next item's start)
+        if (++at.item == items) {
+            at.item = 0;
+            ++at.s;
+            at.span = span_of(p, at.s, false);
+        }
+        at.c = at.span.c0;
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < S - 1; ++i) issue(i);
 
     // ---- one chunk after the other ---------------------------------------------
-    uint32_t q[D / 16][4];
-    float acc[NT][4] = {};
-    float m = -INFINITY, l = 0.f, factor = 0.f;
-    int ref = 0;   // exponent (biased) of the V scales that acc is relative to
-    int parts = 0, cur_s = -1, cur_item = 0;
+    uint2 q[C::kQShared ? 1 : KS][C::kQShared ? 1 : NB];
+    float bias[FMT == kI4 ? D / 32 : 1][NB];   // I4: what the codes' offset of 8 adds to a group's products
+    float acc[NB][KS][4] = {};
+    float m[NB], l[NB], factor[NB];            // of head 4 b + t; l of positions g and g + 8 only, until the segment's end
+#pragma unroll
+    for (int b = 0; b < NB; ++b) m[b] = -FLT_MAX, l[b] = factor[b] = 0.f;
+    int ref = kLeastRef;
+    int cur_s = -1, cur_item = 0;
     bool open = false;   // acc holds a segment that is not its whole item and ends with the share
-    // lane's value e of group i of 8 consecutive elements, and the group's first element
-    auto value = [&](int i, int e) {
-        if (FMT == kI4) return whole(acc[i * 4 + (e & 3)][e >> 2], acc[i * 4 + (e & 3)][2 + (e >> 2)]);
-        if (FMT == kI8 && D == 128) return whole(acc[(i & 1) * 8 + e][i >> 1], acc[(i & 1) * 8 + e][2 + (i >> 1)]);
-        return whole(acc[(i >> 1) * 8 + e][i & 1], acc[(i >> 1) * 8 + e][2 + (i & 1)]);
+    // elements of V in acc[.][i]: rows g and g + 8
+    auto element = [&](int i, int second) {
+        if (FMT == kI8) return 16 * i + 2 * g + second;
+        if (FMT == kI4) return 32 * (i / 2) + 4 * g + 2 * (i & 1) + second;
+        return 16 * i + 8 * second + g;
     };
-    auto place = [&](int i) {
-        if (FMT == kI4) return 32 * i + 8 * t;
-        if (FMT == kI8 && D == 128) return 16 * (2 * t + (i >> 1)) + 8 * (i & 1);
-        return 8 * (2 * t + (i & 1) + 8 * (i >> 1));
-    };
-    // (m, l, o) of this lane's part of head g, as the partial results are kept
-    auto save = [&](float *dst) {
+    // o of a partial result; m and l go to part_m and part_l
+    auto save = [&](float *dst, int slot) {
         const float unit = C::kScale ? pow2_of(ref) * 0x1p-13f : 1.f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            float4 *o = reinterpret_cast<float4 *>(dst + g * D + place(i));
-            o[0] = make_float4(value(i, 0) * unit, value(i, 1) * unit, value(i, 2) * unit, value(i, 3) * unit);
-            o[1] = make_float4(value(i, 4) * unit, value(i, 5) * unit, value(i, 6) * unit, value(i, 7) * unit);
+        for (int b = 0; b < NB; ++b) {
+            float *o = dst + (4 * b + t) * DP;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                o[element(i, 0)] = whole(acc[b][i][0], acc[b][i][1]) * unit;
+                o[element(i, 1)] = whole(acc[b][i][2], acc[b][i][3]) * unit;
+            }
+            if (g == 0) {
+                part_m[slot][4 * b + t] = m[b];
+                part_l[slot][4 * b + t] = l[b];
+            }
         }
-        if (t == 0) {
-            dst[kHeads * D + g] = m;
-            dst[kHeads * D + kHeads + g] = l;
+        if (lane == 0) {
+            part_s[slot] = cur_s;
+            part_item[slot] = cur_item;
         }
     };
     float *warp_part = p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W + warp) * (C::kPart / 4);
+    // this lane's row in loads of four matrices: rows 0-7 and 8-15 of piece 2 i, then of piece 2 i + 1 (K, and V of
+    // 8 and 4 bits), or rows 0-7 of pieces 2 i and 2 i + 1, then rows 8-15 (V of 16 bits)
+    const int mat_row = lane & 15, mat_piece = lane >> 4;
+    const int mat_row_v = C::kF ? (lane & 7) + 8 * (lane >> 4) : mat_row, mat_piece_v = C::kF ? (lane >> 3) & 1 : mat_piece;
 
     int stage = 0;
-    for (long long u = u0; u < u1; ++u, stage = stage + 1 == S ? 0 : stage + 1) {
+#pragma unroll 1
+    for (int u = 0; u < issued; ++u, stage = stage + 1 == S ? 0 : stage + 1) {
         copy_wait<S - 2>();
         __syncwarp();
         issue(stage ? stage - 1 : S - 1);
@@ -427,403 +454,531 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D>::kWarps, 1) k_paged(AttnParam
         if (info.y & kFirst) {
             cur_s = info.z;
             cur_item = info.w;
-            const int head = cur_item % blocks_per_head * kHeads + g;   // in its group
-            const bool live = head < p.group;
-            const long long row = cur_s * p.qs + (long long)(cur_item / blocks_per_head * p.group + head) * D;
-            float v[D / 32][8], top = 0.f;
+            // column g: head g / 2 of each tile, its rounding (g even) or what is left (odd)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int d = FMT == kI4 ? 32 * i + 8 * t : FMT == kI8 ? 16 * (t + 4 * (i >> 1)) + 8 * (i & 1) : 8 * (t + 4 * i);
-                if (live) load8(p.q, row + d, p.dt, v[i]);
+            for (int b = 0; b < NB; ++b) {
+                const int head = cur_item % blocks_per_head * C::kHeads + 4 * b + g / 2;   // in its group
+                const bool live = head < p.group;
+                const long long row = cur_s * p.qs + (long long)(cur_item / blocks_per_head * p.group + head) * D;
+                // the elements at places 2t, 2t + 1, 2t + 8, 2t + 9 of product i
+                auto at_first = [&](int i) { return FMT == kI8 ? 16 * i + 4 * t : FMT == kI4 ? 32 * (i / 2) + 8 * t + 2 * (i & 1) : 16 * i + 2 * t; };
+                constexpr int kSecond = FMT == kI8 ? 2 : FMT == kI4 ? 4 : 8;
+                float2 v[KS][2];
+                float top = 0.f;
+                if (p.dt == kF32) {
+                    const float *src = reinterpret_cast<const float *>(p.q) + (live ? row : 0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!live) v[i][e] = 0.f;
-                    top = fmaxf(top, fabsf(v[i][e]));
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) v[i][h] = *reinterpret_cast<const float2 *>(src + at_first(i) + h * kSecond);
+                } else {
+                    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (live ? row : 0);
+                    uint32_t w[KS][2];
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) w[i][h] = *reinterpret_cast<const uint32_t *>(src + at_first(i) + h * kSecond);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            v[i][h] = p.dt == kF16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i][h]))
+                                                   : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i][h]));
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!live) v[i][h] = make_float2(0.f, 0.f);
+                        top = fmaxf(top, fmaxf(fabsf(v[i][h].x), fabsf(v[i][h].y)));
+                    }
+                // the head's largest element is brought to [1, 2) (I4: 2^8 times that), so that no part leaves the range
+                // of 16 bits
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                const int ex = min(max(__float_as_int(top) >> 23, 16), 253);
+                const float down = pow2_of(254 - ex) * (FMT == kI4 ? 0x1p8f : 1.f);
+                const float f = pow2_of(ex) * (p.softcap > 0.f ? p.scale : p.scale * 1.4426950408889634f) *
+                                (FMT == kI4 ? 0x1p16f : 1.f);   // (codes of 4 bits are n 2^-24)
+                factor[b] = __shfl_sync(~0u, f, 8 * t);          // of head t
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    // (I4: a code's low end holds the even elements, whose queries pair up, and 16 times the odd ones)
+                    const float2 x = FMT == kI4 ? make_float2(v[i][0].x, v[i][1].x) : v[i][0];
+                    const float2 y = FMT == kI4 ? make_float2(v[i][0].y, v[i][1].y) : v[i][1];
+                    const float down2 = FMT == kI4 ? down * 0x1p-4f : down;
+                    const uint2 pair = make_uint2(part_pair<BF>(x.x * down, x.y * down, g & 1), part_pair<BF>(y.x * down2, y.y * down2, g & 1));
+                    if (FMT == kI4) {
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&pair.x));
+                        const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&pair.y));
+                        sum += a.x + a.y + 16.f * (c.x + c.y);
+                    }
+                    if (C::kQShared) q_shared[(i * NB + b) * 32 + lane] = pair;
+                    else q[C::kQShared ? 0 : i][C::kQShared ? 0 : b] = pair;
+                    if (FMT == kI4 && (i & 1)) {
+                        sum += __shfl_xor_sync(~0u, sum, 1);
+                        sum += __shfl_xor_sync(~0u, sum, 2);
+                        sum += __shfl_xor_sync(~0u, sum, 4);
+                        bias[FMT == kI4 ? i / 2 : 0][b] = __shfl_sync(~0u, sum, 8 * t) * -0x1p-21f;
+                        sum = 0.f;
+                    }
+                }
+                m[b] = -FLT_MAX;
+                l[b] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) acc[b][i][0] = acc[b][i][1] = acc[b][i][2] = acc[b][i][3] = 0.f;
+            }
+            ref = kLeastRef;
+            if (C::kQShared) __syncwarp();
+        }
+        auto query = [&](int i, int b) {
+            return C::kQShared ? q_shared[(i * NB + b) * 32 + lane] : q[C::kQShared ? 0 : i][C::kQShared ? 0 : b];
+        };
+
+        // ---- scores of head 4 b + t at positions g and g + 8
+        float x[NB][2];
+        uint2 ks[2], vs[2];   // scales of these positions
+        if (C::kScale) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (FMT == kI8) {
+                    ks[e].x = lds32(base + C::kOffS + (g + 8 * e) * 8);
+                    vs[e].x = lds32(base + C::kOffS + 128 + (g + 8 * e) * 8);
+                } else {
+                    ks[e] = lds64(base + C::kOffS + (g + 8 * e) * 8);
+                    vs[e] = lds64(base + C::kOffS + 128 + (g + 8 * e) * 8);
                 }
             }
-            // the head's largest element is brought to [1, 2), so that no part leaves the range of 16 bits
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const int ex = min(max(__float_as_int(top) >> 23, 1), 253);
-            const float down = pow2_of(254 - ex);
-            factor = pow2_of(ex);
-            factor *= p.softcap > 0.f ? p.scale : p.scale * 1.4426950408889634f;
+        }
+        if (FMT == kI4) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int b = 0; b < NB; ++b) x[b][0] = x[b][1] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] *= down;
-                constexpr int step = FMT == kI4 ? 4 : 1, next = FMT == kI4 ? 1 : 2;
+            for (int i = 0; i < P / 2; ++i) {
+                uint32_t r[4];
+                ldm4<false>(base + 16 * place(mat_row, 2 * i + mat_piece), r);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int e = FMT == kI4 ? 2 * h : 4 * h;
-                    split2<BF>(v[i][e], v[i][e + step], q[2 * i + h][0], q[2 * i + h][1]);
-                    split2<BF>(v[i][e + next], v[i][e + next + step], q[2 * i + h][2], q[2 * i + h][3]);
+                    const int j = 2 * i + h;
+                    const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1], s0 = r0 >> 8, s1 = r1 >> 8;
+                    // a code n at the low end of 16 bits is the number n 2^-24, four bits further up 16 n 2^-24 (the
+                    // queries there are a 16th)
+                    const uint32_t a0[4] = {r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u};
+                    const uint32_t a1[4] = {s0 & 0x000f000fu, s1 & 0x000f000fu, s0 & 0x00f000f0u, s1 & 0x00f000f0u};
+                    const uint32_t k0 = j < 2 ? ks[0].x : ks[0].y, k1 = j < 2 ? ks[1].x : ks[1].y;
+                    const __half2 h0 = *reinterpret_cast<const __half2 *>(&k0), h1 = *reinterpret_cast<const __half2 *>(&k1);
+                    const float f0 = j & 1 ? __high2float(h0) : __low2float(h0), f1 = j & 1 ? __high2float(h1) : __low2float(h1);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float c[4] = {bias[FMT == kI4 ? j : 0][b], 0.f, bias[FMT == kI4 ? j : 0][b], 0.f};
+                        mma<false>(c, a0, query(2 * j, b));
+                        mma<false>(c, a1, query(2 * j + 1, b));
+                        x[b][0] += f0 * (c[0] + c[1]);
+                        x[b][1] += f1 * (c[2] + c[3]);
+                    }
                 }
             }
-            m = -INFINITY;
-            l = 0.f;
-            ref = kLeastRef;
+        } else {
+            constexpr int CH = NB == 1 ? 2 : 1;   // independent sums, where there are few products to fill the pipe with
+            float c[NB][CH][4] = {};
 #pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        }
-
-        // scores of head g at positions 2t, 2t + 1, 8 + 2t, 9 + 2t
-        float x[4];
-        float vs[4] = {};       // I8: V scales of these positions
-        uint2 vs4[4];           // I4: four (two) fp16 scales of each
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (FMT == kI4) {
-                x[2 * h] = x[2 * h + 1] = 0.f;
-                uint2 ks[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    ks[e] = lds64(base + C::kOffS + (8 * h + 2 * t + e) * 8);
-                    vs4[2 * h + e] = lds64(base + C::kOffS + (16 + 8 * h + 2 * t + e) * 8);
-                }
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const int key = g + 8 * h;
-                    constexpr int P = C::kRow / 16;
-                    const uint32_t w = lds32(base + key * C::kRow + 16 * (j ^ ((key >> (P == 4 ? 1 : 2)) & (P - 1))) + 4 * t);
-                    uint32_t b[4];
-                    nibbles(w, b);
-                    float c[4] = {};
-                    mma<false>(c, q[2 * j], b[0], b[1]);
-                    mma<false>(c, q[2 * j + 1], b[2], b[3]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t u2 = j < 2 ? ks[e].x : ks[e].y;
-                        const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&u2));
-                        x[2 * h + e] += (j & 1 ? sc.y : sc.x) * (c[e] + c[2 + e]);
-                    }
-                }
-            } else {
-                float c[4] = {};
-                constexpr int JK = C::kRow / 64;
-#pragma unroll
-                for (int j = 0; j < JK; ++j) {
-                    const uint4 w = lds128(base + (h * JK + j) * 512 + lane * 16);
-                    if (FMT == kI8) {
-                        const uint32_t u4[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma<false>(c, q[j * 4 + i], bytes01(u4[i]), bytes23(u4[i]));
-                    } else {
-                        mma<BF>(c, q[2 * j], w.x, w.y);
-                        mma<BF>(c, q[2 * j + 1], w.z, w.w);
-                    }
-                }
-                x[2 * h] = C::kF ? whole(c[0], c[2]) : c[0] + c[2];
-                x[2 * h + 1] = C::kF ? whole(c[1], c[3]) : c[1] + c[3];
+            for (int i = 0; i < KS; ++i) {
                 if (FMT == kI8) {
+                    if (i & 1) continue;
+                    uint32_t r[4];
+                    ldm4<false>(base + 16 * place(mat_row, i + mat_piece), r);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[2 * h + e] *= __uint_as_float(lds32(base + C::kOffS + (8 * h + 2 * t + e) * 8));
-                        vs[2 * h + e] = __uint_as_float(lds32(base + C::kOffS + (16 + 8 * h + 2 * t + e) * 8));
+                    for (int e = 0; e < 4; ++e) r[e] ^= 0x80808080u;
+                    const uint32_t a0[4] = {bytes<0x4140>(r[0]), bytes<0x4140>(r[1]), bytes<0x4342>(r[0]), bytes<0x4342>(r[1])};
+                    const uint32_t a1[4] = {bytes<0x4140>(r[2]), bytes<0x4140>(r[3]), bytes<0x4342>(r[2]), bytes<0x4342>(r[3])};
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        mma<false>(c[b][0], a0, query(i, b));
+                        mma<false>(c[b][CH - 1], a1, query(i + 1 < KS ? i + 1 : i, b));
                     }
+                } else {
+                    uint32_t r[4];
+                    ldm4<false>(base + 16 * place(mat_row, 2 * i + mat_piece), r);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mma<BF>(c[b][i % CH], r, query(i, b));
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (CH == 2) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[b][0][e] += c[b][CH - 1][e];
+                }
+                x[b][0] = C::kF ? whole(c[b][0][0], c[b][0][1]) : c[b][0][0] + c[b][0][1];
+                x[b][1] = C::kF ? whole(c[b][0][2], c[b][0][3]) : c[b][0][2] + c[b][0][3];
+                if (FMT == kI8) {
+                    x[b][0] *= __uint_as_float(ks[0].x);
+                    x[b][1] *= __uint_as_float(ks[1].x);
                 }
             }
         }
+        bool grows = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] *= factor;
-            if (p.softcap > 0.f) {   // cap * tanh(x / cap) = cap - 2 cap / (1 + e^(2x / cap))
-                const float z = exp2_(x[e] * (2.8853900817779268f / p.softcap));
-                x[e] = (p.softcap - 2.f * p.softcap / (1.f + z)) * 1.4426950408889634f;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float &y = x[b][e];
+                y *= factor[b];
+                if (p.softcap > 0.f) {   // cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap))
+                    const float z = exp2_(y * (2.8853900817779268f / p.softcap));
+                    y = (p.softcap - 2.f * p.softcap / (1.f + z)) * 1.4426950408889634f;
+                }
+                if (!((mask >> (g + 8 * e)) & 1)) y = -INFINITY;
+                grows |= y > m[b];   // (a NaN is passed over here and makes l and o NaN below)
             }
-        }
-        if (mask != 0xffffu) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!((mask >> (2 * t + (e & 1) + 8 * (e >> 1))) & 1)) x[e] = -INFINITY;
-        }
-        // the running maximum (a NaN score is passed over here and makes l and o NaN below)
-        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        top = fmaxf(top, m);
         int big = 0;   // exponent of the largest V scale
         if (FMT == kI8) {
-            big = __float_as_int(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]))) >> 23;
+            big = __float_as_int(fmaxf(__uint_as_float(vs[0].x), __uint_as_float(vs[1].x))) >> 23;
         } else if (FMT == kI4) {
-            __half2 hm = *reinterpret_cast<const __half2 *>(&vs4[0].x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                hm = __hmax2(hm, *reinterpret_cast<const __half2 *>(&vs4[e].x));
-                if (D == 128) hm = __hmax2(hm, *reinterpret_cast<const __half2 *>(&vs4[e].y));
-            }
+            __half2 hm = __hmax2(*reinterpret_cast<const __half2 *>(&vs[0].x), *reinterpret_cast<const __half2 *>(&vs[1].x));
+            if (D == 128)
+                hm = __hmax2(hm, __hmax2(*reinterpret_cast<const __half2 *>(&vs[0].y), *reinterpret_cast<const __half2 *>(&vs[1].y)));
             big = __float_as_int(__half2float(__hmax(__low2half(hm), __high2half(hm)))) >> 23;
         }
-        const float zero = top == -INFINITY ? 0.f : top;
-        if (__any_sync(~0u, top != m || big > ref)) {
-            int grown = ref;
+        if (__any_sync(~0u, grows || (C::kScale && big > ref))) {
+            float both = 1.f;
             if (C::kScale) {
                 if (FMT == kI4 && big == 255) {   // an infinite scale spoils its own group only: the largest of the others
                     big = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int i = 0; i < D / 64; ++i) {
-                            const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(i ? &vs4[e].y : &vs4[e].x));
+                            const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(i ? &vs[e].y : &vs[e].x));
                             if (sc.x < INFINITY) big = max(big, __float_as_int(sc.x) >> 23);
                             if (sc.y < INFINITY) big = max(big, __float_as_int(sc.y) >> 23);
                         }
                 }
-                big = max(big, __shfl_xor_sync(~0u, big, 1));
-                big = max(big, __shfl_xor_sync(~0u, big, 2));
-                grown = max(ref, min(big, 253));
+                const int grown = min(int(__reduce_max_sync(~0u, unsigned(max(ref, big)))), 253);
+                both = grown - ref > 126 ? 0.f : pow2_of(127 + ref - grown);   // 2^(ref - grown); beyond floats' range 0
+                ref = grown;
             }
-            const float shrink = exp2_(m - zero);
-            // 2^(ref - grown); a difference beyond the range of floats is 0
-            const float both = shrink * (grown - ref > 126 ? 0.f : pow2_of(127 + ref - grown));
-            l *= shrink;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                acc[i][0] *= both;
-                acc[i][1] *= both;
-                acc[i][2] *= both;
-                acc[i][3] *= both;
-            }
-            m = top;
-            ref = grown;
-        }
-        float w[4];
+            for (int b = 0; b < NB; ++b) {
+                float top = fmaxf(m[b], fmaxf(x[b][0], x[b][1]));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+                const float shrink = exp2_(m[b] - top), f = shrink * both;
+                l[b] *= shrink;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // F16: weights carry a factor 2^14, so that the low parts of small ones stay normal numbers
-            w[e] = exp2_(FMT == kF16 ? x[e] - zero + 14.f : x[e] - zero);
-            l += w[e];
-        }
-        if (C::kF) {
-            uint32_t a[4];
-            split2<BF>(w[0], w[1], a[0], a[1]);
-            split2<BF>(w[2], w[3], a[2], a[3]);
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                uint4 r[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = lds128(base + C::kOffV + (i * (D / 64) + j) * 512 + lane * 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t r0 = (&r[0].x)[i], r1 = (&r[1].x)[i], r2 = (&r[2].x)[i], r3 = (&r[3].x)[i];
-                    mma<BF>(acc[j * 8 + 2 * i], a, __byte_perm(r0, r1, 0x5410), __byte_perm(r2, r3, 0x5410));
-                    mma<BF>(acc[j * 8 + 2 * i + 1], a, __byte_perm(r0, r1, 0x7632), __byte_perm(r2, r3, 0x7632));
+                for (int i = 0; i < KS; ++i) {
+                    acc[b][i][0] *= f;
+                    acc[b][i][1] *= f;
+                    acc[b][i][2] *= f;
+                    acc[b][i][3] *= f;
                 }
+                m[b] = top;
             }
-        } else if (FMT == kI8) {
-            const float f = pow2_of(254 - ref) * 0x1p13f;
-            uint32_t a[4];
-            split2<false>(w[0] * (vs[0] * f), w[1] * (vs[1] * f), a[0], a[1]);
-            split2<false>(w[2] * (vs[2] * f), w[3] * (vs[3] * f), a[2], a[3]);
-            constexpr int WORDS = D / 32;   // 4 (16 bytes of a row for each lane) or 2
-            uint32_t r[4][WORDS];
+        }
+        // ---- weights
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (WORDS == 4) {
-                    const uint4 v = lds128(base + C::kOffV + i * 512 + lane * 16);
-                    r[i][0] = v.x, r[i][1] = v.y, r[i][WORDS - 2] = v.z, r[i][WORDS - 1] = v.w;
-                } else {
-                    const uint2 v = lds64(base + C::kOffV + i * 256 + lane * 8);
-                    r[i][0] = v.x, r[i][1] = v.y;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // F16: weights carry a factor 2^14, so that the low parts of small ones stay normal numbers
+                x[b][e] = exp2_(FMT == kF16 ? x[b][e] - m[b] + 14.f : x[b][e] - m[b]);
+                l[b] += x[b][e];
+            }
+        // ---- sums of V
+        const float f = pow2_of(254 - ref) * 0x1p13f;
+        if (FMT == kI4) {
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+                uint32_t r[4];
+                ldm4<true>(base + C::kOffV + 16 * place(mat_row, 2 * i + mat_piece), r);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = 2 * i + h;
+                    // element 4 g + e of positions 2t, 2t + 1 at bits 4 e: under the exponent of 1024 a code is 1024 + n
+                    // or 1024 + 16 n; less 8 these are exact
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const uint32_t w = r[2 * h + o], z = w >> 8;
+                        a[0][2 * o] = hsub((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        a[0][2 * o + 1] = hfma((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+                        a[1][2 * o] = hsub((z & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        a[1][2 * o + 1] = hfma((z & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+                    }
+                    const uint32_t k0 = j < 2 ? vs[0].x : vs[0].y, k1 = j < 2 ? vs[1].x : vs[1].y;
+                    const __half2 h0 = *reinterpret_cast<const __half2 *>(&k0), h1 = *reinterpret_cast<const __half2 *>(&k1);
+                    const float f0 = f * (j & 1 ? __high2float(h0) : __low2float(h0));
+                    const float f1 = f * (j & 1 ? __high2float(h1) : __low2float(h1));
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint2 w = make_uint2(transpose8(split<false>(x[b][0] * f0)), transpose8(split<false>(x[b][1] * f1)));
+                        mma<false>(acc[b][2 * j], a[0], w);
+                        mma<false>(acc[b][2 * j + 1], a[1], w);
+                    }
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) {
-                const uint32_t r0 = r[0][i] ^ 0x80808080u, r1 = r[1][i] ^ 0x80808080u, r2 = r[2][i] ^ 0x80808080u,
-                               r3 = r[3][i] ^ 0x80808080u;
-                const uint32_t a01 = __byte_perm(r0, r1, 0x5140), a23 = __byte_perm(r0, r1, 0x7362);
-                const uint32_t b01 = __byte_perm(r2, r3, 0x5140), b23 = __byte_perm(r2, r3, 0x7362);
-                mma<false>(acc[4 * i], a, bytes01(a01), bytes01(b01));
-                mma<false>(acc[4 * i + 1], a, bytes23(a01), bytes23(b01));
-                mma<false>(acc[4 * i + 2], a, bytes01(a23), bytes01(b23));
-                mma<false>(acc[4 * i + 3], a, bytes23(a23), bytes23(b23));
             }
         } else {
-            const float f = pow2_of(254 - ref) * 0x1p13f;
-            constexpr int P = C::kRow / 16;
-            const uint32_t pick = g & 1 ? 0x7632 : 0x5410;
+            uint2 w[NB];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] *= f;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                float v[4];
-                uint32_t r[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = 2 * t + (e & 1) + 8 * (e >> 1);
-                    const uint32_t u2 = j < 2 ? vs4[e].x : vs4[e].y;
-                    const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&u2));
-                    v[e] = w[e] * (j & 1 ? sc.y : sc.x);
-                    r[e] = lds32(base + C::kOffV + key * C::kRow + 16 * (j ^ ((key >> (P == 4 ? 1 : 2)) & (P - 1))) + 4 * (g >> 1));
+            for (int b = 0; b < NB; ++b) {
+                if (FMT == kI8) {
+                    x[b][0] *= __uint_as_float(vs[0].x) * f;
+                    x[b][1] *= __uint_as_float(vs[1].x) * f;
                 }
-                uint32_t a[4], b0[4], b1[4];
-                split2<false>(v[0], v[1], a[0], a[1]);
-                split2<false>(v[2], v[3], a[2], a[3]);
-                nibbles(__byte_perm(r[0], r[1], pick), b0);
-                nibbles(__byte_perm(r[2], r[3], pick), b1);
+                w[b] = make_uint2(transpose8(split<BF>(x[b][0])), transpose8(split<BF>(x[b][1])));
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma<false>(acc[4 * j + i], a, b0[i], b1[i]);
+            for (int i = 0; i < KS; ++i) {
+                uint32_t r[4];
+                if (FMT == kI8) {
+                    if (i & 1) continue;
+                    ldm4<true>(base + C::kOffV + 16 * place(mat_row_v, i + mat_piece_v), r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] ^= 0x80808080u;
+                    // elements 2g and 2g + 1 of positions 2t, 2t + 1 in turn
+                    const uint32_t a0[4] = {bytes<0x4240>(r[0]), bytes<0x4341>(r[0]), bytes<0x4240>(r[1]), bytes<0x4341>(r[1])};
+                    const uint32_t a1[4] = {bytes<0x4240>(r[2]), bytes<0x4341>(r[2]), bytes<0x4240>(r[3]), bytes<0x4341>(r[3])};
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        mma<false>(acc[b][i], a0, w[b]);
+                        mma<false>(acc[b][i + 1 < KS ? i + 1 : i], a1, w[b]);
+                    }
+                } else {
+                    ldm4<true>(base + C::kOffV + 16 * place(mat_row_v, 2 * i + mat_piece_v), r);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mma<BF>(acc[b][i], r, w[b]);
+                }
             }
         }
 
         if (info.y & kLast) {
-            l += __shfl_xor_sync(~0u, l, 1);
-            l += __shfl_xor_sync(~0u, l, 2);
-            if (FMT == kF16) l *= 0x1p-14f;
-            if (FMT == kF16) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    acc[i][0] *= 0x1p-14f;
-                    acc[i][1] *= 0x1p-14f;
-                    acc[i][2] *= 0x1p-14f;
-                    acc[i][3] *= 0x1p-14f;
+            for (int b = 0; b < NB; ++b) {
+                l[b] += __shfl_xor_sync(~0u, l[b], 4);
+                l[b] += __shfl_xor_sync(~0u, l[b], 8);
+                l[b] += __shfl_xor_sync(~0u, l[b], 16);
+                if (FMT == kF16) {
+                    l[b] *= 0x1p-14f;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        acc[b][i][0] *= 0x1p-14f;
+                        acc[b][i][1] *= 0x1p-14f;
+                        acc[b][i][2] *= 0x1p-14f;
+                        acc[b][i][3] *= 0x1p-14f;
+                    }
                 }
             }
             if (info.y & kWhole) {
-                const int hb = cur_item % blocks_per_head * kHeads + g;
-                if (hb < p.group) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int hb = cur_item % blocks_per_head * C::kHeads + 4 * b + t;
+                    if (hb >= p.group) continue;
                     const int head = cur_item / blocks_per_head * p.group + hb;
-                    const float unit = (l == 0.f ? 0.f : 1.f / l) * (C::kScale ? pow2_of(ref) * 0x1p-13f : 1.f);
+                    const float unit = (l[b] == 0.f ? 0.f : 1.f / l[b]) * (C::kScale ? pow2_of(ref) * 0x1p-13f : 1.f);
+                    const long long o = cur_s * p.os + (long long)head * D;
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        float o[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = value(i, e) * unit;
-                        store8(p.out, cur_s * p.os + (long long)head * D + place(i), p.dt, o);
+                    for (int i = 0; i < KS; ++i) {
+                        output(p.out, o + element(i, 0), p.dt, whole(acc[b][i][0], acc[b][i][1]) * unit);
+                        output(p.out, o + element(i, 1), p.dt, whole(acc[b][i][2], acc[b][i][3]) * unit);
                     }
-                    if (p.lse && t == 0)
-                        p.lse[(long long)cur_s * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    if (p.lse && g == 0)
+                        p.lse[(long long)cur_s * p.heads + head] = l[b] == 0.f ? -INFINITY : (m[b] + log2f(l[b])) * 0.6931471805599453f;
                 }
             } else {
-                if (u + 1 < u1) save(warp_part);   // more follows: the first partial result leaves by way of L2
+                if (u + 1 < issued) save(warp_part, 2 * warp);   // more follows: the first partial result leaves by way of L2
                 else open = true;
-                if (lane == 0) {
-                    part_s[warp][open ? 1 : 0] = cur_s;
-                    part_item[warp][open ? 1 : 0] = cur_item;
-                }
-                ++parts;
             }
         }
     }
     copy_wait<0>();
-    __syncthreads();   // every ring is empty
-    if (open) save(reinterpret_cast<float *>(ring));
+    __syncwarp();      // the warp's ring is empty
+    if (open) save(reinterpret_cast<float *>(ring), 2 * warp + 1);
     __syncthreads();
 
-    // ---- partial results of the CTA's warps, item by item ---------------------------
-    auto part_of = [&](int i) {   // contribution i: warp i / 2, its first or its last
-        return i & 1 ? reinterpret_cast<const float *>(smem + (i / 2) * C::kRing)
-                     : p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W + i / 2) * (C::kPart / 4);
-    };
-    constexpr int EL = kHeads * D / (32 * W);          // consecutive elements of a thread
-    static_assert(EL == 2 || EL == 4, "");
-    const int e0 = threadIdx.x * EL, h = e0 / D;
-    // joins (pm, pl, po) of one contribution to the thread's sums
-    auto join = [&](float &jm, float &jl, float (&jo)[EL], const float *src, bool far) {
-        const float pm = far ? __ldcg(src + kHeads * D + h) : src[kHeads * D + h];
-        const float pl = far ? __ldcg(src + kHeads * D + kHeads + h) : src[kHeads * D + kHeads + h];
-        float po[EL];
-#pragma unroll
-        for (int e = 0; e < EL; e += 2) {
-            const float2 v = far ? __ldcg(reinterpret_cast<const float2 *>(src + e0 + e)) : *reinterpret_cast<const float2 *>(src + e0 + e);
-            po[e] = v.x;
-            po[e + 1] = v.y;
+    // ---- partial results of the CTA's warps, joined for each of their items ---------
+    if (warp == 0) {   // one lane for each slot: the first slot of an item's run makes its entry
+        const int s = lane < 2 * W ? part_s[lane] : -1, item = s >= 0 ? part_item[lane] : 0;
+        const unsigned valid = __ballot_sync(~0u, s >= 0), before = valid & ((1u << lane) - 1);
+        const int prev = before ? 31 - __clz(before) : lane;
+        const int ps = __shfl_sync(~0u, s, prev), pi = __shfl_sync(~0u, item, prev);
+        const bool head = s >= 0 && (!before || ps != s || pi != item);
+        const unsigned heads = __ballot_sync(~0u, head);
+        if (head) {
+            Joint &j = joints[__popc(heads & ((1u << lane) - 1))];
+            const unsigned later = heads & ~((2u << lane) - 1);
+            j.s = s;
+            j.item = item;
+            j.slots = valid & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : ~0u);
+            long long start = offs[s / per];
+            for (int r = s / per * per; r < s; ++r) {
+                const Span sp = span_of(p, r, false);
+                start += (long long)(sp.c1 - sp.c0 + 1) * items;
+            }
+            const Span sp = span_of(p, s, false);
+            const int nc = sp.c1 - sp.c0;
+            start += (long long)item * (nc + 1);
+            j.a = shares.of(start + 1) / W;   // CTAs of its first and last chunk
+            j.b = shares.of(start + nc) / W;
         }
-        const float nm = fmaxf(jm, pm), zero = nm == -INFINITY ? 0.f : nm;
-        const float a = exp2_(jm - zero), b = exp2_(pm - zero);
-        jl = jl * a + pl * b;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) jo[e] = jo[e] * a + po[e] * b;
-        jm = nm;
+        if (lane == 0) n_joints = __popc(heads);
+    }
+    __syncthreads();
+    const int nj = n_joints;
+    auto part_of = [&](int slot) {
+        return slot & 1 ? reinterpret_cast<const float *>(smem + (slot / 2) * C::kRing)
+                        : p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W + slot / 2) * (C::kPart / 4);
     };
-    auto finish = [&](int s, int item, float jm, float jl, const float (&jo)[EL]) {
-        const int hb = item % blocks_per_head * kHeads + h;
+    // this CTA's partial results of items that others share: 2 CTA for one that began before it, 2 CTA + 1 for one
+    // that begins in it
+    auto far_of = [&](int cta, const Joint &j) { return p.part + (size_t)(2 * cta + (cta == j.a)) * (C::kPart / 4); };
+    auto finish = [&](const Joint &j, int h, int d, float jm, float jl, float jo) {
+        const int hb = j.item % blocks_per_head * C::kHeads + h;
         if (hb >= p.group) return;
-        const int head = item / blocks_per_head * p.group + hb;
-        const float unit = jl == 0.f ? 0.f : 1.f / jl;
-        const long long i = s * p.os + (long long)head * D + e0 % D;
-#pragma unroll
-        for (int e = 0; e < EL; e += 2) {
-            if (p.dt == kF32) *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + i + e) = make_float2(jo[e] * unit, jo[e + 1] * unit);
-            else *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + i + e) = pack2(jo[e] * unit, jo[e + 1] * unit, p.dt);
-        }
-        if (p.lse && e0 % D == 0)
-            p.lse[(long long)s * p.heads + head] = jl == 0.f ? -INFINITY : (jm + log2f(jl)) * 0.6931471805599453f;
+        const int head = j.item / blocks_per_head * p.group + hb;
+        output(p.out, j.s * p.os + (long long)head * D + d, p.dt, jl == 0.f ? 0.f : jo / jl);
+        if (p.lse && d == 0)
+            p.lse[(long long)j.s * p.heads + head] = jl == 0.f ? -INFINITY : (jm + log2f(jl)) * 0.6931471805599453f;
     };
-    for (int i = 0; i < 2 * W;) {
-        const int s = part_s[i / 2][i & 1];
-        if (s < 0) {
-            ++i;
-            continue;
+    // weights of the slots, by (item, head); the sums m and l take the place of the first slot's
+    for (int e = threadIdx.x; e < nj * C::kHeads; e += T) {
+        const int h = e % C::kHeads;
+        const unsigned slots = joints[e / C::kHeads].slots;
+        float jm = -FLT_MAX, jl = 0.f;
+        for (unsigned k = slots; k; k &= k - 1) jm = fmaxf(jm, part_m[__ffs(k) - 1][h]);
+        for (unsigned k = slots; k; k &= k - 1) {
+            const int i = __ffs(k) - 1;
+            const float f = exp2_(part_m[i][h] - jm);
+            part_f[i][h] = f;
+            jl += f * part_l[i][h];
         }
-        const int item = part_item[i / 2][i & 1];
-        float jm = -INFINITY, jl = 0.f, jo[EL] = {};
-        int j = i;
-        for (; j < 2 * W; ++j) {
-            const int s2 = part_s[j / 2][j & 1];
-            if (s2 < 0) continue;
-            if (s2 != s || part_item[j / 2][j & 1] != item) break;
-            join(jm, jl, jo, part_of(j), !(j & 1));
-        }
-        i = j;
-        // the item's chunks, and whether they are all in this CTA
-        long long start = offs[s / per];
-        for (int r = s / per * per; r < s; ++r) {
-            const Span sp = span_of(p, r, false);
-            start += (long long)(sp.c1 - sp.c0) * items;
-        }
-        const Span sp = span_of(p, s, false);
-        const int nc = sp.c1 - sp.c0;
-        start += (long long)item * nc;
-        const long long end = start + nc;
-        if (start >= cta0 && end <= cta1) {
-            finish(s, item, jm, jl, jo);
-            continue;
-        }
-        const int a = int(((start + 1) * ctas - 1) / total), b = int((end * ctas - 1) / total);   // CTAs of its first and last chunk
-        // slots: 2 CTA for an item that began before the CTA (or fills it), 2 CTA + 1 for one that begins in it
-        float *dst = p.part + (size_t)(2 * blockIdx.x + (int(blockIdx.x) == a)) * (C::kPart / 4);
+        part_m[__ffs(slots) - 1][h] = jm;
+        part_l[__ffs(slots) - 1][h] = jl;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < nj * C::kHeads * D; e += T) {
+        const Joint &j = joints[e / (C::kHeads * D)];
+        const int h = e / D % C::kHeads, d = e % D, first_slot = __ffs(j.slots) - 1;
+        float jo = 0.f;
+        for (unsigned k = j.slots; k;) {   // four slots at a time
+            float v[4], f[4];
 #pragma unroll
-        for (int e = 0; e < EL; e += 2) *reinterpret_cast<float2 *>(dst + e0 + e) = make_float2(jo[e], jo[e + 1]);
-        if (e0 % D == 0) {
-            dst[kHeads * D + h] = jm;
-            dst[kHeads * D + kHeads + h] = jl;
+            for (int i = 0; i < 4; ++i) {
+                const int slot = k ? __ffs(k) - 1 : first_slot;
+                v[i] = part_of(slot)[h * DP + d];
+                f[i] = part_f[slot][h];
+                if (!k) v[i] = f[i] = 0.f;
+                k &= k - 1;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) jo += f[i] * v[i];
         }
+        const float jm = part_m[first_slot][h], jl = part_l[first_slot][h];
+        if (j.a == j.b) {
+            finish(j, h, d, jm, jl, jo);
+        } else {
+            float *dst = far_of(blockIdx.x, j);
+            dst[h * DP + d] = jo;
+            if (d == 0) {
+                dst[C::kHeads * DP + h] = jm;
+                dst[C::kHeads * (DP + 1) + h] = jl;
+            }
+        }
+    }
+    // ---- items that CTAs share: the CTA that is through last joins their results (its first and last item at most) ---
+    if (nj == 0 || (joints[0].a == joints[0].b && joints[nj - 1].a == joints[nj - 1].b)) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        const Joint &j = joints[threadIdx.x ? nj - 1 : 0];
+        bool all = false;
+        if (j.a != j.b && (threadIdx.x == 0 || nj > 1)) {
+            all = atomicAdd(p.tickets + j.a, 1u) == unsigned(j.b - j.a);
+            if (all) p.tickets[j.a] = 0;   // zero again for the next call
+        }
+        last[threadIdx.x] = all;
+    }
+    __syncthreads();
+    float *far_m = reinterpret_cast<float *>(smem), *far_l = far_m + gridDim.x * C::kHeads;   // over the rings
+    constexpr int E4 = C::kHeads * D / 4, G = T > E4 ? T / E4 : 1;   // threads of a result, groups of them
+    float4 *far_o = reinterpret_cast<float4 *>(smem + 32 * 1024);
+    for (int i = 0; i < 2; ++i) {
+        if (!last[i]) continue;
+        const Joint j = joints[i ? nj - 1 : 0];
+        const int nc = j.b - j.a + 1;
         __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const bool all = atomicAdd(p.tickets + a, 1u) == unsigned(b - a);
-            if (all) p.tickets[a] = 0;   // zero again for the next call
-            is_last = all;
+        for (int e = threadIdx.x; e < nc * C::kHeads; e += T) {
+            const float *src = far_of(j.a + e / C::kHeads, j) + C::kHeads * DP + e % C::kHeads;
+            far_m[e] = __ldcg(src);
+            far_l[e] = __ldcg(src + C::kHeads);
         }
         __syncthreads();
-        if (is_last) {
-            __threadfence();
-            jm = -INFINITY;
-            jl = 0.f;
+        const int grp = threadIdx.x / E4;
+        for (int e = threadIdx.x % E4; e < E4; e += G > 1 ? E4 : T) {
+            const int h = 4 * e / D, d = 4 * e % D;
+            float jm = -FLT_MAX, jl = 0.f;
+            for (int c = 0; c < nc; ++c) jm = fmaxf(jm, far_m[c * C::kHeads + h]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int c = G > 1 ? grp : 0; c < nc; c += G) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(far_of(j.a + c, j) + h * DP + d));
+                const float f = exp2_(far_m[c * C::kHeads + h] - jm);
+                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+            }
+            if (G > 1) {
+                far_o[threadIdx.x] = o;
+                continue;
+            }
+            for (int c = 0; c < nc; ++c) jl += exp2_(far_m[c * C::kHeads + h] - jm) * far_l[c * C::kHeads + h];
+            finish(j, h, d, jm, jl, o.x);
+            finish(j, h, d + 1, jm, jl, o.y);
+            finish(j, h, d + 2, jm, jl, o.z);
+            finish(j, h, d + 3, jm, jl, o.w);
+        }
+        __syncthreads();
+        if constexpr (G > 1) {
+            for (int e = threadIdx.x; e < C::kHeads * D; e += T) {
+                const int h = e / D, d = e % D;
+                float jm = -FLT_MAX, jl = 0.f, jo = 0.f;
+                for (int c = 0; c < nc; ++c) jm = fmaxf(jm, far_m[c * C::kHeads + h]);
+                for (int c = 0; c < nc; ++c) jl += exp2_(far_m[c * C::kHeads + h] - jm) * far_l[c * C::kHeads + h];
 #pragma unroll
-            for (int e = 0; e < EL; ++e) jo[e] = 0.f;
-            for (int c = a; c <= b; ++c) join(jm, jl, jo, p.part + (size_t)(2 * c + (c == a)) * (C::kPart / 4), true);
-            finish(s, item, jm, jl, jo);
+                for (int k = 0; k < G; ++k) jo += reinterpret_cast<const float *>(far_o + k * E4)[e];
+                finish(j, h, d, jm, jl, jo);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
-template <int FMT, int D>
+// Query heads that share a cached head are taken 4, 8 or 16 at a time.
+int tiles_of(int group) { return group <= 4 ? 1 : group <= 8 ? 2 : 4; }
+
+template <int FMT, int D, int NB>
 cudaError_t launch(const AttnParams &p, cudaStream_t st, bool set)
 {
-    using C = Cfg<FMT, D>;
-    if (set) return cudaFuncSetAttribute(k_paged<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    const int blocks = (p.group + kHeads - 1) / kHeads;
-    k_paged<FMT, D><<<p.n_sm, 32 * C::kWarps, C::kSmem, st>>>(p, p.kv_heads * blocks, blocks);
+    using C = Cfg<FMT, D, NB>;
+    if (set) return cudaFuncSetAttribute(k_paged<FMT, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const int blocks = (p.group + C::kHeads - 1) / C::kHeads;
+    k_paged<FMT, D, NB><<<p.n_sm, 32 * C::kWarps, C::kSmem, st>>>(p, p.kv_heads * blocks, blocks);
     return cudaGetLastError();
+}
+
+template <int FMT, int D>
+cudaError_t by_group(const AttnParams &p, cudaStream_t st, bool set)
+{
+    switch (tiles_of(p.group)) {
+    case 1: return launch<FMT, D, 1>(p, st, set);
+    case 2: return launch<FMT, D, 2>(p, st, set);
+    default: return launch<FMT, D, 4>(p, st, set);
+    }
 }
 
 template <int FMT>
 cudaError_t by_dim(const AttnParams &p, cudaStream_t st, bool set)
 {
-    return p.dim == 128 ? launch<FMT, 128>(p, st, set) : launch<FMT, 64>(p, st, set);
+    return p.dim == 128 ? by_group<FMT, 128>(p, st, set) : by_group<FMT, 64>(p, st, set);
 }
 
 cudaError_t dispatch(const AttnParams &p, cudaStream_t st, bool set)
@@ -838,20 +993,26 @@ cudaError_t dispatch(const AttnParams &p, cudaStream_t st, bool set)
 
 }  // namespace
 
-// 2 partial results for each CTA, then one for each warp
-size_t attn_part_bytes(int n_sm) { return size_t(n_sm) * (2 + kMaxWarps) * Cfg<kF16, 128>::kPart; }
+// 2 partial results for each CTA, then one for each of its warps (16 at most)
+size_t attn_part_bytes(int n_sm, int group)
+{
+    const int nb = tiles_of(group);
+    return size_t(n_sm) * 18 * (nb == 1 ? Cfg<kF16, 128, 1>::kPart : nb == 2 ? Cfg<kF16, 128, 2>::kPart : Cfg<kF16, 128, 4>::kPart);
+}
 size_t attn_ticket_bytes(int n_sm) { return size_t(n_sm) * sizeof(unsigned); }
 
 cudaError_t attn_setup()
 {
     AttnParams p{};
     for (int fmt : {int(kF16), int(kBF16), int(kI8), int(kI4)})
-        for (int dim : {64, 128}) {
-            p.c.fmt = fmt;
-            p.dim = dim;
-            const cudaError_t e = dispatch(p, nullptr, true);
-            if (e != cudaSuccess) return e;
-        }
+        for (int dim : {64, 128})
+            for (int group : {4, 8, 16}) {
+                p.c.fmt = fmt;
+                p.dim = dim;
+                p.group = group;
+                const cudaError_t e = dispatch(p, nullptr, true);
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 
