@@ -436,6 +436,9 @@ pi_status pi_paged_attention(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_
     pi_status st = cache_view(a, cache, table, p.c);
     if (st != PI_OK) return st;
     const int b = bytes_of(dtype), qlen = D.n_heads * D.head_dim, n = table->n_seqs;
+    if ((long long)n * ((long long)table->width * D.page_size / 16 + 3) * D.n_kv_heads * pi::attn_blocks(D.n_heads / D.n_kv_heads) >
+        (1LL << 30))
+        return fail(PI_ERR_INVALID_ARG, "page table: n_seqs * width * page_size * n_kv_heads is above 2^34 (2^30 tiles of work)");
     p.qs = q_stride;
     p.os = out_stride;
     st = check_rows("q", q_dev, p.qs, qlen, b, n);

@@ -81,6 +81,7 @@ struct AttnParams {
     int *err;
     int n_sm;
 };
+int attn_blocks(int group);   // blocks of query heads that share a cached head
 size_t attn_part_bytes(int n_sm, int group);
 size_t attn_ticket_bytes(int n_sm);
 cudaError_t attn_setup();   // once per device, before any launch

@@ -27,6 +27,7 @@ namespace pi {
 namespace {
 
 constexpr int kChunk = 16;            // positions
+constexpr int kSlots = 32;            // partial results of a CTA's warps, at most (2 for each)
 
 // FMT: the cache's format.  NB: tiles of 4 query heads that share a cached head.
 template <int FMT, int D, int NB>
@@ -40,17 +41,18 @@ struct Cfg {
     static constexpr int kStage = kOffI + 16;
     static constexpr int kHeads = 4 * NB;                                     // query heads of an item
     static constexpr int kStep = D / 16;                                      // products of 16 along the head
-    static constexpr bool kQShared = NB * D >= 512;                           // queries in shared memory, not registers
-    static constexpr int kQ = kQShared ? kStep * NB * 256 : 0;
-    // Warps of a CTA: 16 where 128 registers do; 16-bit rows of 256 bytes leave room for three stages of 8 warps.
-    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : 8) : NB * D <= 128 ? 16 : 8;
+    static constexpr bool kQShared = NB * D >= 512;                           // queries stay in shared memory
     static constexpr int kDP = D + 8;                                         // a head's distance in a partial result
     static constexpr int kPart = kHeads * (kDP + 2) * 4;                      // its bytes: o, then m and l
-    static constexpr int kRoom = 220 * 1024 / kWarps;
-    static constexpr int kStages = (kRoom - kQ) / kStage < 8 ? (kRoom - kQ) / kStage : 8;
+    static constexpr int kBuf = kHeads * (kDP + 8) * 4;                       // a warp's: queries, later its result
+    // Warps of a CTA: as many as registers and three stages each allow.
+    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : NB == 2 ? 6 : 8) : NB * D == 64 ? 16 : NB * D == 128 ? 12 : 8;
+    static constexpr int kRoom = 220 * 1024 / kWarps / 16 * 16;
+    static constexpr int kStages = (kRoom - kBuf) / kStage < 8 ? (kRoom - kBuf) / kStage : 8;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kSmem = kWarps * (kRing + kQ);
-    static_assert(kStages >= 3 && kRing >= kPart && kPart % 16 == 0 && kRing % 16 == 0 && kSmem + 8448 <= 227 * 1024, "");
+    static constexpr int kSmem = kWarps * (kRing + kBuf);
+    static_assert(kStages >= 3 && kBuf % 16 == 0 && kRing % 16 == 0 && kSmem + 7168 <= 227 * 1024, "");
+    static_assert(kBuf >= kHeads * kDP * 4 + kHeads * (1 + D / 32) * 4 && 16 * D * NB <= kHeads * kDP * 4, "");
 };
 
 __device__ __forceinline__ uint32_t s2u(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -152,20 +154,20 @@ __device__ __forceinline__ uint32_t hfma(uint32_t v, uint32_t a, uint32_t b)
 template <uint32_t SEL>
 __device__ __forceinline__ uint32_t bytes(uint32_t w) { return hsub(__byte_perm(w, 0x64646464u, SEL), 0x64806480u); }
 
-// Two numbers' 16-bit roundings, or (low) the roundings of what is left.
+// Two numbers' 16-bit roundings, and the roundings of what is left.
 template <bool BF>
-__device__ __forceinline__ uint32_t part_pair(float a, float b, bool low)
+__device__ __forceinline__ uint2 split2(float a, float b)
 {
     if (BF) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         const float2 f = __bfloat1622float2(h);
         const __nv_bfloat162 l = __floats2bfloat162_rn(a - f.x, b - f.y);
-        return low ? *reinterpret_cast<const uint32_t *>(&l) : *reinterpret_cast<const uint32_t *>(&h);
+        return make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l));
     }
     const __half2 h = __floats2half2_rn(a, b);
     const float2 f = __half22float2(h);
     const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-    return low ? *reinterpret_cast<const uint32_t *>(&l) : *reinterpret_cast<const uint32_t *>(&h);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l));
 }
 __device__ __forceinline__ void output(uint8_t *p, long long i, int dt, float v)
 {
@@ -173,6 +175,25 @@ __device__ __forceinline__ void output(uint8_t *p, long long i, int dt, float v)
     else if (dt == kF16) reinterpret_cast<__half *>(p)[i] = __float2half(v);
     else reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v);
 }
+
+// Eight consecutive results from shared memory.
+__device__ __forceinline__ void output8(uint8_t *p, long long i, int dt, const float *v)
+{
+    const float4 a = *reinterpret_cast<const float4 *>(v), b = *reinterpret_cast<const float4 *>(v + 4);
+    if (dt == kF32) {
+        reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i)[0] = a;
+        reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i)[1] = b;
+    } else if (dt == kF16) {
+        const __half2 h[4] = {__floats2half2_rn(a.x, a.y), __floats2half2_rn(a.z, a.w), __floats2half2_rn(b.x, b.y), __floats2half2_rn(b.z, b.w)};
+        *reinterpret_cast<uint4 *>(p + 2 * i) = *reinterpret_cast<const uint4 *>(h);
+    } else {
+        const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w), __floats2bfloat162_rn(b.x, b.y),
+                                     __floats2bfloat162_rn(b.z, b.w)};
+        *reinterpret_cast<uint4 *>(p + 2 * i) = *reinterpret_cast<const uint4 *>(h);
+    }
+}
+// log of sum l at maximum m (a power of two's exponents); -infinity without any position.
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
 
 // Positions of one sequence that its query sees, and the chunks that hold them.
 // A sequence with none has one chunk without positions, whose result is 0.
@@ -195,23 +216,19 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int s, bool report)
     return r;
 }
 
-// A quotient of numbers >= 0: 32-bit arithmetic where it will do (a 64-bit division takes some 100 cycles more).
-__device__ __forceinline__ long long quotient(long long a, long long b)
-{
-    return (a | b) >> 31 ? a / b : (long long)(unsigned(a) / unsigned(b));
-}
-
 // The work of a call in units: one for each chunk, and one before each item, for
-// its start (queries, the result).  Warp `share` of `shares` takes the units from
-// first(share) up to first(share + 1).
+// its start (queries, the result).  CTA c takes the units from first(c) up to
+// first(c + 1): an even share, and item by item where all items are alike and
+// the CTAs a multiple of them.
 struct Shares {
-    long long each, more;   // units of every share, shares that have one more
-    __device__ Shares(long long total, int shares) : each(quotient(total, shares)), more(total - each * shares) {}
-    __device__ long long first(long long share) const { return share * each + min(share, more); }
-    __device__ int of(long long unit) const
+    int total, ctas, each, more;
+    __device__ Shares(int total_, int ctas_) : total(total_), ctas(ctas_), each(unsigned(total_) / unsigned(ctas_)), more(total_ - each * ctas_) {}
+    __device__ int first(int c) const { return c * each + int(unsigned(c * more) / unsigned(ctas)); }
+    __device__ int of(int unit) const
     {
-        const long long big = more * (each + 1);
-        return int(unit < big ? quotient(unit, each + 1) : more + quotient(unit - big, each));   // (each > 0 if unit >= big)
+        int c = int(float(unit) * (float(ctas) / float(total)));   // off by one at most
+        if (first(c) > unit) --c;
+        return first(c + 1) <= unit ? c + 1 : c;
     }
 };
 
@@ -243,34 +260,36 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 {
     using C = Cfg<FMT, D, NB>;
     constexpr bool BF = FMT == kBF16;
-    constexpr int W = C::kWarps, S = C::kStages, T = 32 * W, KS = C::kStep, P = C::kPieces, DP = C::kDP;
+    constexpr int W = C::kWarps, S = C::kStages, T = 32 * W, KS = C::kStep, P = C::kPieces, DP = C::kDP, H = C::kHeads;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long sums[W];
-    __shared__ long long offs[T];
-    // partial results: slot 2 w of warp w's first segment (in global memory), 2 w + 1 of its last (in its ring)
-    __shared__ int part_s[2 * W], part_item[2 * W];
-    __shared__ float part_m[2 * W][C::kHeads], part_l[2 * W][C::kHeads], part_f[2 * W][C::kHeads];
+    __shared__ int sums[W], offs[T];
+    // partial results: slot 2 w of warp w's first segment (in global memory), 2 w + 1 of its last (in its buffer)
+    __shared__ int part_s[kSlots], part_item[kSlots];
+    __shared__ float part_m[2 * W][H], part_l[2 * W][H];
     __shared__ Joint joints[2 * W];
     __shared__ int n_joints, last[2];
+    __shared__ float2 joint_of[H];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int n = p.c.n_seqs;
 
     // ---- units before each thread's block of sequences --------------------
     const int per = (n + T - 1) / T;
-    long long mine = 0;
+    int mine = 0;
+#pragma unroll 1
     for (int s = threadIdx.x * per; s < min(n, (int(threadIdx.x) + 1) * per); ++s) {
         const Span r = span_of(p, s, blockIdx.x == 0);
-        mine += (long long)(r.c1 - r.c0 + 1) * items;
+        mine += (r.c1 - r.c0 + 1) * items;
     }
-    long long scan = mine;
+    int scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(~0u, scan, o);
+        const int v = __shfl_up_sync(~0u, scan, o);
         if (lane >= o) scan += v;
     }
     if (lane == 31) sums[warp] = scan;
+    if (threadIdx.x < kSlots) part_s[threadIdx.x] = -1;
     __syncthreads();
-    long long total = 0, before = 0;
+    int total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         before += w < warp ? sums[w] : 0;
@@ -280,16 +299,16 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     __syncthreads();
 
     // ---- this warp's share ---------------------------------------------------
-    const long long want = (total + W - 1) / W;
-    const int ctas = int(want < gridDim.x ? want : gridDim.x);   // at least a unit for each warp
+    int ctas = min((total + W - 1) / W, int(gridDim.x));   // at least a unit for each warp
+    if (n == 1 && 4 * items <= int(gridDim.x)) ctas = max(ctas / items, 1) * items;   // no CTA with parts of two items
     if (int(blockIdx.x) >= ctas) return;
-    const Shares shares(total, ctas * W);
-    const long long u0 = shares.first(blockIdx.x * W + warp);
-    int left = int(shares.first(blockIdx.x * W + warp + 1) - u0);   // units not yet taken
+    const Shares shares(total, ctas);
+    const int cta0 = shares.first(blockIdx.x), units = shares.first(blockIdx.x + 1) - cta0;
+    const int u0 = cta0 + units * warp / W;
+    int left = cta0 + units * (warp + 1) / W - u0;   // units not yet taken
     uint8_t *ring = smem + warp * C::kRing;
     const uint32_t ring_u = s2u(ring);
-    uint2 *q_shared = reinterpret_cast<uint2 *>(smem + W * C::kRing + warp * C::kQ);
-    if (lane < 2) part_s[2 * warp + lane] = -1;
+    float *buf = reinterpret_cast<float *>(smem + W * C::kRing + warp * C::kBuf);
 
     Cursor at{};
     if (left > 0) {
@@ -300,17 +319,17 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             else end = mid;
         }
         at.s = b * per;
-        long long rest = u0 - offs[b];
+        int rest = u0 - offs[b];
         for (;;) {
             at.span = span_of(p, at.s, false);
-            const long long here = (long long)(at.span.c1 - at.span.c0 + 1) * items;
+            const int here = (at.span.c1 - at.span.c0 + 1) * items;
             if (rest < here) break;
             rest -= here;
             ++at.s;
         }
         const int nu = at.span.c1 - at.span.c0 + 1;
-        at.item = int(quotient(rest, nu));
-        const int unit = int(rest - (long long)at.item * nu);   // 0: the item's start
+        at.item = unsigned(rest) / unsigned(nu);
+        const int unit = rest - at.item * nu;   // 0: the item's start
         if (unit == 0) --left;
         at.c = at.span.c0 + max(unit - 1, 0);
     }
@@ -320,7 +339,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     auto place = [](int r, int i) { return r * P + (i ^ (P >= 8 ? r & 7 : P == 4 ? (r >> 1) & 3 : (r >> 2) & 1)); };
     constexpr int RI = 32 / P;            // rows of one copy instruction
     const int my_row = lane / P, my_piece = lane % P;
-    const long long slot_bytes = (long long)p.c.slot_rows * C::kRow, scale_slot = (long long)p.c.slot_rows * C::kScale;
+    const unsigned slot_bytes = p.c.slot_rows * C::kRow, scale_slot = p.c.slot_rows * C::kScale;   // 2^18 at most
     // Pages of both halves of chunk page_c + lane of sequence page_s.
     int page_s = -1, page_c = 0, page_a = -1, page_b = -1;
     int issued = 0;
@@ -352,27 +371,24 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             if (lane == 0) atomicExch(p.err, int(kDevCheck));
             mask &= 0x00ffu;
         }
-        const int sm = p.c.page_size - 1;
-        const long long head = (long long)(at.item / blocks_per_head) * p.c.head_rows;
-        const long long ra = (mask & 0x00ffu) ? (long long)pa * p.c.page_rows + (long long)(pos & sm) * p.c.slot_rows + head : 0;
-        const long long rb = (mask & 0xff00u) ? (long long)pb * p.c.page_rows + (long long)((pos + 8) & sm) * p.c.slot_rows + head : 0;
+        // first rows of the halves; a row without a position is filled with zeros (its memory is not read)
+        const int in_page = pos & (p.c.page_size - 1), in_page_b = (pos + 8) & (p.c.page_size - 1);
+        const int head = at.item / blocks_per_head * p.c.head_rows;
+        const long long ra = (mask & 0x00ffu) ? (long long)pa * p.c.page_rows + (in_page * p.c.slot_rows + head) : 0;
+        const long long rb = (mask & 0xff00u) ? (long long)pb * p.c.page_rows + (in_page_b * p.c.slot_rows + head) : 0;
         const uint32_t dst = ring_u + stage * C::kStage;
-        // a row without a position is filled with zeros (its memory is not read)
 #pragma unroll
         for (int i = 0; i < kChunk / RI; ++i) {
             const int row = my_row + i * RI;
-            const bool live = (mask >> row) & 1;
-            const long long off = (row < 8 ? ra : rb) * C::kRow + (live ? (row & 7) * slot_bytes : 0) + 16 * my_piece;
+            const long long off = (row < 8 ? ra : rb) * C::kRow + ((row & 7) * slot_bytes + 16 * my_piece);
             const uint32_t to = dst + 16 * place(row, my_piece);
-            copy_async<16>(to, p.c.k + off, live);
-            copy_async<16>(to + C::kOffV, p.c.v + off, live);
+            copy_async<16>(to, p.c.k + off, (mask >> row) & 1);
+            copy_async<16>(to + C::kOffV, p.c.v + off, (mask >> row) & 1);
         }
         if (C::kScale) {   // lanes 0-15: K of position lane, 16-31: V
             const int key = lane & 15;
-            const bool live = (mask >> key) & 1;
-            const uint8_t *base = (lane < 16 ? p.c.ks : p.c.vs) + (key < 8 ? ra : rb) * C::kScale +
-                                  (live ? (key & 7) * scale_slot : 0);
-            copy_async<C::kScale ? C::kScale : 4>(dst + C::kOffS + lane * 8, base, live);
+            const uint8_t *base = (lane < 16 ? p.c.ks : p.c.vs) + (key < 8 ? ra : rb) * C::kScale + (key & 7) * scale_slot;
+            copy_async<C::kScale ? C::kScale : 4>(dst + C::kOffS + lane * 8, base, (mask >> key) & 1);
         }
         copy_commit();
         // what the reader has to know
@@ -396,9 +412,6 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         }
         at.c = at.span.c0;
     };
-#pragma unroll 1
-    for (int i = 0; i < S - 1; ++i) issue(i);
-
     // ---- one chunk after the other ---------------------------------------------
     uint2 q[C::kQShared ? 1 : KS][C::kQShared ? 1 : NB];
     float bias[FMT == kI4 ? D / 32 : 1][NB];   // I4: what the codes' offset of 8 adds to a group's products
@@ -408,33 +421,11 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     for (int b = 0; b < NB; ++b) m[b] = -FLT_MAX, l[b] = factor[b] = 0.f;
     int ref = kLeastRef;
     int cur_s = -1, cur_item = 0;
-    bool open = false;   // acc holds a segment that is not its whole item and ends with the share
     // elements of V in acc[.][i]: rows g and g + 8
     auto element = [&](int i, int second) {
         if (FMT == kI8) return 16 * i + 2 * g + second;
         if (FMT == kI4) return 32 * (i / 2) + 4 * g + 2 * (i & 1) + second;
         return 16 * i + 8 * second + g;
-    };
-    // o of a partial result; m and l go to part_m and part_l
-    auto save = [&](float *dst, int slot) {
-        const float unit = C::kScale ? pow2_of(ref) * 0x1p-13f : 1.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float *o = dst + (4 * b + t) * DP;
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                o[element(i, 0)] = whole(acc[b][i][0], acc[b][i][1]) * unit;
-                o[element(i, 1)] = whole(acc[b][i][2], acc[b][i][3]) * unit;
-            }
-            if (g == 0) {
-                part_m[slot][4 * b + t] = m[b];
-                part_l[slot][4 * b + t] = l[b];
-            }
-        }
-        if (lane == 0) {
-            part_s[slot] = cur_s;
-            part_item[slot] = cur_item;
-        }
     };
     float *warp_part = p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W + warp) * (C::kPart / 4);
     // this lane's row in loads of four matrices: rows 0-7 and 8-15 of piece 2 i, then of piece 2 i + 1 (K, and V of
@@ -442,98 +433,127 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     const int mat_row = lane & 15, mat_piece = lane >> 4;
     const int mat_row_v = C::kF ? (lane & 7) + 8 * (lane >> 4) : mat_row, mat_piece_v = C::kF ? (lane >> 3) & 1 : mat_piece;
 
-    int stage = 0;
+    int stage = 0, put = 0;
 #pragma unroll 1
-    for (int u = 0; u < issued; ++u, stage = stage + 1 == S ? 0 : stage + 1) {
-        copy_wait<S - 2>();
-        __syncwarp();
-        issue(stage ? stage - 1 : S - 1);
+    for (int u = 1 - S; u < issued; ++u) {
+        if (u >= 0) {
+            copy_wait<S - 2>();
+            __syncwarp();
+        }
+        issue(put);
+        put = put + 1 == S ? 0 : put + 1;
+        if (u < 0) continue;
         const uint32_t base = ring_u + stage * C::kStage;
         const int4 info = *reinterpret_cast<const int4 *>(ring + stage * C::kStage + C::kOffI);
         const unsigned mask = unsigned(info.x);
         if (info.y & kFirst) {
             cur_s = info.z;
             cur_item = info.w;
-            // column g: head g / 2 of each tile, its rounding (g even) or what is left (odd)
-#pragma unroll
+            // The queries' parts go to the buffer as the products take them: word (i, b, column 4 lanes, t) holds column
+            // g's parts of places 2t, 2t + 1 and 2t + 8, 2t + 9 of product i.  Eight lanes share a head here.
+            uint32_t *words = reinterpret_cast<uint32_t *>(buf);
+            float *extra = buf + H * DP;   // factors, then biases
+            const int hl = lane / 8, part = lane % 8;
+#pragma unroll 1
             for (int b = 0; b < NB; ++b) {
-                const int head = cur_item % blocks_per_head * C::kHeads + 4 * b + g / 2;   // in its group
+                constexpr int E = D / 8;   // elements of a lane: part E, ...
+                const int head = cur_item % blocks_per_head * H + 4 * b + hl;   // in its group
                 const bool live = head < p.group;
-                const long long row = cur_s * p.qs + (long long)(cur_item / blocks_per_head * p.group + head) * D;
-                // the elements at places 2t, 2t + 1, 2t + 8, 2t + 9 of product i
-                auto at_first = [&](int i) { return FMT == kI8 ? 16 * i + 4 * t : FMT == kI4 ? 32 * (i / 2) + 8 * t + 2 * (i & 1) : 16 * i + 2 * t; };
-                constexpr int kSecond = FMT == kI8 ? 2 : FMT == kI4 ? 4 : 8;
-                float2 v[KS][2];
-                float top = 0.f;
+                const long long row = live ? cur_s * p.qs + (long long)(cur_item / blocks_per_head * p.group + head) * D : 0;
+                float v[E], top = 0.f;
                 if (p.dt == kF32) {
-                    const float *src = reinterpret_cast<const float *>(p.q) + (live ? row : 0);
+                    const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + row + part * E);
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) v[i][h] = *reinterpret_cast<const float2 *>(src + at_first(i) + h * kSecond);
+                    for (int i = 0; i < E / 4; ++i) {
+                        const float4 x = src[i];
+                        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                    }
                 } else {
-                    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (live ? row : 0);
-                    uint32_t w[KS][2];
+                    const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + row + part * E);
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
+                    for (int i = 0; i < E / 8; ++i) {
+                        const uint4 x = src[i];
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) w[i][h] = *reinterpret_cast<const uint32_t *>(src + at_first(i) + h * kSecond);
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            v[i][h] = p.dt == kF16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i][h]))
-                                                   : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i][h]));
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = p.dt == kF16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[e]))
+                                                          : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
+                            v[8 * i + 2 * e] = f.x;
+                            v[8 * i + 2 * e + 1] = f.y;
+                        }
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < KS; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!live) v[i][h] = make_float2(0.f, 0.f);
-                        top = fmaxf(top, fmaxf(fabsf(v[i][h].x), fabsf(v[i][h].y)));
-                    }
+                for (int e = 0; e < E; ++e) {
+                    if (!live) v[e] = 0.f;
+                    top = fmaxf(top, fabsf(v[e]));
+                }
                 // the head's largest element is brought to [1, 2) (I4: 2^8 times that), so that no part leaves the range
                 // of 16 bits
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
                 const int ex = min(max(__float_as_int(top) >> 23, 16), 253);
                 const float down = pow2_of(254 - ex) * (FMT == kI4 ? 0x1p8f : 1.f);
-                const float f = pow2_of(ex) * (p.softcap > 0.f ? p.scale : p.scale * 1.4426950408889634f) *
-                                (FMT == kI4 ? 0x1p16f : 1.f);   // (codes of 4 bits are n 2^-24)
-                factor[b] = __shfl_sync(~0u, f, 8 * t);          // of head t
+                if (part == 0)
+                    extra[4 * b + hl] = pow2_of(ex) * (p.softcap > 0.f ? p.scale : p.scale * 1.4426950408889634f) *
+                                        (FMT == kI4 ? 0x1p16f : 1.f);   // (codes of 4 bits are n 2^-24)
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    // (I4: a code's low end holds the even elements, whose queries pair up, and 16 times the odd ones)
-                    const float2 x = FMT == kI4 ? make_float2(v[i][0].x, v[i][1].x) : v[i][0];
-                    const float2 y = FMT == kI4 ? make_float2(v[i][0].y, v[i][1].y) : v[i][1];
-                    const float down2 = FMT == kI4 ? down * 0x1p-4f : down;
-                    const uint2 pair = make_uint2(part_pair<BF>(x.x * down, x.y * down, g & 1), part_pair<BF>(y.x * down2, y.y * down2, g & 1));
+                for (int e = 0; e < E / 2; ++e) {   // a pair of elements, its product i, its place: word x or y of lanes 4 g + tt
+                    const int d = part * E + 2 * e;
+                    float x, y;
+                    int i, tt, second;
+                    if (FMT == kI4) {   // of 8 elements (0, 4), (1, 5), (2, 6), (3, 7); codes of odd ones are 16 times theirs
+                        const int at8 = 8 * (e / 4), k = e % 4;
+                        x = v[at8 + k] * (k & 1 ? down * 0x1p-4f : down);
+                        y = v[at8 + k + 4] * (k & 1 ? down * 0x1p-4f : down);
+                        i = d / 32 * 2 + (k >> 1);
+                        tt = d / 8 % 4;
+                        second = k & 1;
+                    } else {
+                        x = v[2 * e] * down;
+                        y = v[2 * e + 1] * down;
+                        i = d / 16;
+                        tt = FMT == kI8 ? d / 4 % 4 : d / 2 % 4;
+                        second = FMT == kI8 ? d / 2 % 2 : d / 8 % 2;
+                    }
+                    const uint2 w = split2<BF>(x, y);
+                    uint32_t *to = words + (((i * NB + b) * 8 + 2 * hl) * 4 + tt) * 2 + second;
+                    to[0] = w.x;
+                    to[8] = w.y;
                     if (FMT == kI4) {
-                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&pair.x));
-                        const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&pair.y));
-                        sum += a.x + a.y + 16.f * (c.x + c.y);
+                        const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+                        const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+                        sum += ((hi.x + hi.y) + (lo.x + lo.y)) * (e & 1 ? 16.f : 1.f);
                     }
-                    if (C::kQShared) q_shared[(i * NB + b) * 32 + lane] = pair;
-                    else q[C::kQShared ? 0 : i][C::kQShared ? 0 : b] = pair;
-                    if (FMT == kI4 && (i & 1)) {
-                        sum += __shfl_xor_sync(~0u, sum, 1);
-                        sum += __shfl_xor_sync(~0u, sum, 2);
-                        sum += __shfl_xor_sync(~0u, sum, 4);
-                        bias[FMT == kI4 ? i / 2 : 0][b] = __shfl_sync(~0u, sum, 8 * t) * -0x1p-21f;
-                        sum = 0.f;
-                    }
+                }
+                if (FMT == kI4) {   // what the codes' offset of 8 adds to a group's products
+                    sum += __shfl_xor_sync(~0u, sum, 1);
+                    if (E == 8) sum += __shfl_xor_sync(~0u, sum, 2);
+                    if (part % (32 / E) == 0) extra[H + part * E / 32 * H + 4 * b + hl] = sum * -0x1p-21f;
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                factor[b] = extra[4 * b + t];
+                if (FMT == kI4) {
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) bias[FMT == kI4 ? j : 0][b] = extra[H + j * H + 4 * b + t];
                 }
                 m[b] = -FLT_MAX;
                 l[b] = 0.f;
 #pragma unroll
-                for (int i = 0; i < KS; ++i) acc[b][i][0] = acc[b][i][1] = acc[b][i][2] = acc[b][i][3] = 0.f;
+                for (int i = 0; i < KS; ++i) {
+                    if (!C::kQShared) q[C::kQShared ? 0 : i][C::kQShared ? 0 : b] = reinterpret_cast<const uint2 *>(buf)[(i * NB + b) * 32 + lane];
+                    acc[b][i][0] = acc[b][i][1] = acc[b][i][2] = acc[b][i][3] = 0.f;
+                }
             }
             ref = kLeastRef;
-            if (C::kQShared) __syncwarp();
         }
         auto query = [&](int i, int b) {
-            return C::kQShared ? q_shared[(i * NB + b) * 32 + lane] : q[C::kQShared ? 0 : i][C::kQShared ? 0 : b];
+            return C::kQShared ? reinterpret_cast<const uint2 *>(buf)[(i * NB + b) * 32 + lane] : q[C::kQShared ? 0 : i][C::kQShared ? 0 : b];
         };
 
         // ---- scores of head 4 b + t at positions g and g + 8
@@ -753,53 +773,61 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             }
         }
 
-        if (info.y & kLast) {
+        if (info.y & kLast) {   // o to the buffer, one row for each head
+            if (C::kQShared) __syncwarp();
+            const bool whole_item = info.y & kWhole, more = u + 1 < issued;
+            const int slot = 2 * warp + !more;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 l[b] += __shfl_xor_sync(~0u, l[b], 4);
                 l[b] += __shfl_xor_sync(~0u, l[b], 8);
                 l[b] += __shfl_xor_sync(~0u, l[b], 16);
-                if (FMT == kF16) {
-                    l[b] *= 0x1p-14f;
+                float unit = C::kScale ? pow2_of(ref) * 0x1p-13f : FMT == kF16 ? 0x1p-14f : 1.f;
+                if (FMT == kF16) l[b] *= 0x1p-14f;
+                if (whole_item) unit = l[b] == 0.f ? 0.f : unit / l[b];
+                float *o = buf + (4 * b + t) * DP;
 #pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        acc[b][i][0] *= 0x1p-14f;
-                        acc[b][i][1] *= 0x1p-14f;
-                        acc[b][i][2] *= 0x1p-14f;
-                        acc[b][i][3] *= 0x1p-14f;
-                    }
+                for (int i = 0; i < KS; ++i) {
+                    o[element(i, 0)] = whole(acc[b][i][0], acc[b][i][1]) * unit;
+                    o[element(i, 1)] = whole(acc[b][i][2], acc[b][i][3]) * unit;
+                }
+                if (g == 0 && !whole_item) {
+                    part_m[slot][4 * b + t] = m[b];
+                    part_l[slot][4 * b + t] = l[b];
+                }
+                if (g == 0 && whole_item && p.lse) {
+                    const int hb = cur_item % blocks_per_head * H + 4 * b + t;
+                    if (hb < p.group) p.lse[(long long)cur_s * p.heads + cur_item / blocks_per_head * p.group + hb] = lse_of(m[b], l[b]);
                 }
             }
-            if (info.y & kWhole) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int hb = cur_item % blocks_per_head * C::kHeads + 4 * b + t;
-                    if (hb >= p.group) continue;
-                    const int head = cur_item / blocks_per_head * p.group + hb;
-                    const float unit = (l[b] == 0.f ? 0.f : 1.f / l[b]) * (C::kScale ? pow2_of(ref) * 0x1p-13f : 1.f);
-                    const long long o = cur_s * p.os + (long long)head * D;
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        output(p.out, o + element(i, 0), p.dt, whole(acc[b][i][0], acc[b][i][1]) * unit);
-                        output(p.out, o + element(i, 1), p.dt, whole(acc[b][i][2], acc[b][i][3]) * unit);
-                    }
-                    if (p.lse && g == 0)
-                        p.lse[(long long)cur_s * p.heads + head] = l[b] == 0.f ? -INFINITY : (m[b] + log2f(l[b])) * 0.6931471805599453f;
-                }
+            __syncwarp();
+            if (whole_item) {
+                const int hb0 = cur_item % blocks_per_head * H;
+                const long long row = cur_s * p.os + (long long)(cur_item / blocks_per_head * p.group + hb0) * D;
+                const int end = min(p.group - hb0, H) * D;
+#pragma unroll 1
+                for (int e = 8 * lane; e < end; e += 256) output8(p.out, row + e, p.dt, buf + e / D * DP + e % D);
             } else {
-                if (u + 1 < issued) save(warp_part, 2 * warp);   // more follows: the first partial result leaves by way of L2
-                else open = true;
+                if (lane == 0) {
+                    part_s[slot] = cur_s;
+                    part_item[slot] = cur_item;
+                }
+                if (more) {   // the first partial result makes room by way of L2
+#pragma unroll 1
+                    for (int e = 4 * lane; e < H * DP; e += 128)
+                        *reinterpret_cast<float4 *>(warp_part + e) = *reinterpret_cast<const float4 *>(buf + e);
+                }
             }
+            __syncwarp();
         }
+        stage = stage + 1 == S ? 0 : stage + 1;
     }
     copy_wait<0>();
-    __syncwarp();      // the warp's ring is empty
-    if (open) save(reinterpret_cast<float *>(ring), 2 * warp + 1);
     __syncthreads();
 
     // ---- partial results of the CTA's warps, joined for each of their items ---------
     if (warp == 0) {   // one lane for each slot: the first slot of an item's run makes its entry
-        const int s = lane < 2 * W ? part_s[lane] : -1, item = s >= 0 ? part_item[lane] : 0;
+        const int s = part_s[lane], item = s >= 0 ? part_item[lane] : 0;
         const unsigned valid = __ballot_sync(~0u, s >= 0), before = valid & ((1u << lane) - 1);
         const int prev = before ? 31 - __clz(before) : lane;
         const int ps = __shfl_sync(~0u, s, prev), pi = __shfl_sync(~0u, item, prev);
@@ -811,78 +839,83 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             j.s = s;
             j.item = item;
             j.slots = valid & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : ~0u);
-            long long start = offs[s / per];
+            int start = offs[s / per];
             for (int r = s / per * per; r < s; ++r) {
                 const Span sp = span_of(p, r, false);
-                start += (long long)(sp.c1 - sp.c0 + 1) * items;
+                start += (sp.c1 - sp.c0 + 1) * items;
             }
             const Span sp = span_of(p, s, false);
             const int nc = sp.c1 - sp.c0;
-            start += (long long)item * (nc + 1);
-            j.a = shares.of(start + 1) / W;   // CTAs of its first and last chunk
-            j.b = shares.of(start + nc) / W;
+            start += item * (nc + 1);
+            j.a = shares.of(start + 1);   // CTAs of its first and last chunk
+            j.b = shares.of(start + nc);
         }
         if (lane == 0) n_joints = __popc(heads);
     }
     __syncthreads();
     const int nj = n_joints;
     auto part_of = [&](int slot) {
-        return slot & 1 ? reinterpret_cast<const float *>(smem + (slot / 2) * C::kRing)
+        return slot & 1 ? reinterpret_cast<const float *>(smem + W * C::kRing + (slot / 2) * C::kBuf)
                         : p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W + slot / 2) * (C::kPart / 4);
     };
     // this CTA's partial results of items that others share: 2 CTA for one that began before it, 2 CTA + 1 for one
     // that begins in it
-    auto far_of = [&](int cta, const Joint &j) { return p.part + (size_t)(2 * cta + (cta == j.a)) * (C::kPart / 4); };
+    auto far_of = [&](int cta, int a) { return p.part + (size_t)(2 * cta + (cta == a)) * (C::kPart / 4); };
+    // an item's results leave with o as it is, or divided by l
     auto finish = [&](const Joint &j, int h, int d, float jm, float jl, float jo) {
-        const int hb = j.item % blocks_per_head * C::kHeads + h;
+        const int hb = j.item % blocks_per_head * H + h;
         if (hb >= p.group) return;
         const int head = j.item / blocks_per_head * p.group + hb;
         output(p.out, j.s * p.os + (long long)head * D + d, p.dt, jl == 0.f ? 0.f : jo / jl);
-        if (p.lse && d == 0)
-            p.lse[(long long)j.s * p.heads + head] = jl == 0.f ? -INFINITY : (jm + log2f(jl)) * 0.6931471805599453f;
+        if (p.lse && d == 0) p.lse[(long long)j.s * p.heads + head] = lse_of(jm, jl);
     };
-    // weights of the slots, by (item, head); the sums m and l take the place of the first slot's
-    for (int e = threadIdx.x; e < nj * C::kHeads; e += T) {
-        const int h = e % C::kHeads;
-        const unsigned slots = joints[e / C::kHeads].slots;
+    // weights of the slots by (item, head) in place of their m; the sums m and l in the rings, which are empty
+    float *joint_m = reinterpret_cast<float *>(smem), *joint_l = joint_m + 2 * W * H;
+    for (int e = threadIdx.x; e < nj * H; e += T) {
+        const int h = e % H;
+        const unsigned slots = joints[e / H].slots;
         float jm = -FLT_MAX, jl = 0.f;
+#pragma unroll 1
         for (unsigned k = slots; k; k &= k - 1) jm = fmaxf(jm, part_m[__ffs(k) - 1][h]);
+#pragma unroll 1
         for (unsigned k = slots; k; k &= k - 1) {
             const int i = __ffs(k) - 1;
             const float f = exp2_(part_m[i][h] - jm);
-            part_f[i][h] = f;
+            part_m[i][h] = f;
             jl += f * part_l[i][h];
         }
-        part_m[__ffs(slots) - 1][h] = jm;
-        part_l[__ffs(slots) - 1][h] = jl;
+        joint_m[e] = jm;
+        joint_l[e] = jl;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < nj * C::kHeads * D; e += T) {
-        const Joint &j = joints[e / (C::kHeads * D)];
-        const int h = e / D % C::kHeads, d = e % D, first_slot = __ffs(j.slots) - 1;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < nj * H * D; e += T) {
+        const Joint &j = joints[e / (H * D)];
+        const int h = e / D % H, d = e % D, first_slot = __ffs(j.slots) - 1;
         float jo = 0.f;
+#pragma unroll 1
         for (unsigned k = j.slots; k;) {   // four slots at a time
             float v[4], f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int slot = k ? __ffs(k) - 1 : first_slot;
                 v[i] = part_of(slot)[h * DP + d];
-                f[i] = part_f[slot][h];
+                f[i] = part_m[slot][h];
                 if (!k) v[i] = f[i] = 0.f;
                 k &= k - 1;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) jo += f[i] * v[i];
         }
-        const float jm = part_m[first_slot][h], jl = part_l[first_slot][h];
+        const float jm = joint_m[e / D], jl = joint_l[e / D];
         if (j.a == j.b) {
             finish(j, h, d, jm, jl, jo);
         } else {
-            float *dst = far_of(blockIdx.x, j);
+            float *dst = far_of(blockIdx.x, j.a);
             dst[h * DP + d] = jo;
             if (d == 0) {
-                dst[C::kHeads * DP + h] = jm;
-                dst[C::kHeads * (DP + 1) + h] = jl;
+                dst[H * DP + h] = jm;
+                dst[H * (DP + 1) + h] = jl;
             }
         }
     }
@@ -900,55 +933,61 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         last[threadIdx.x] = all;
     }
     __syncthreads();
-    float *far_m = reinterpret_cast<float *>(smem), *far_l = far_m + gridDim.x * C::kHeads;   // over the rings
-    constexpr int E4 = C::kHeads * D / 4, G = T > E4 ? T / E4 : 1;   // threads of a result, groups of them
+    // far_f: weights; far_o: sums of the thread groups
+    float *far_f = reinterpret_cast<float *>(smem), *far_l = far_f + gridDim.x * H;
+    constexpr int E4 = H * D / 4, G = T > E4 ? T / E4 : 1;   // threads of a result, groups of them
     float4 *far_o = reinterpret_cast<float4 *>(smem + 32 * 1024);
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         if (!last[i]) continue;
         const Joint j = joints[i ? nj - 1 : 0];
         const int nc = j.b - j.a + 1;
         __threadfence();
-        for (int e = threadIdx.x; e < nc * C::kHeads; e += T) {
-            const float *src = far_of(j.a + e / C::kHeads, j) + C::kHeads * DP + e % C::kHeads;
-            far_m[e] = __ldcg(src);
-            far_l[e] = __ldcg(src + C::kHeads);
+        for (int e = threadIdx.x; e < nc * H; e += T) {
+            const float *src = far_of(j.a + e / H, j.a) + H * DP + e % H;
+            far_f[e] = __ldcg(src);
+            far_l[e] = __ldcg(src + H);
         }
         __syncthreads();
-        const int grp = threadIdx.x / E4;
-        for (int e = threadIdx.x % E4; e < E4; e += G > 1 ? E4 : T) {
-            const int h = 4 * e / D, d = 4 * e % D;
+        // a warp for each head: the maximum, the weights, the sum
+        for (int h = warp; h < H; h += W) {
             float jm = -FLT_MAX, jl = 0.f;
-            for (int c = 0; c < nc; ++c) jm = fmaxf(jm, far_m[c * C::kHeads + h]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = G > 1 ? grp : 0; c < nc; c += G) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(far_of(j.a + c, j) + h * DP + d));
-                const float f = exp2_(far_m[c * C::kHeads + h] - jm);
-                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+            for (int c = lane; c < nc; c += 32) jm = fmaxf(jm, far_f[c * H + h]);
+            for (int o = 16; o; o >>= 1) jm = fmaxf(jm, __shfl_xor_sync(~0u, jm, o));
+            for (int c = lane; c < nc; c += 32) {
+                const float f = exp2_(far_f[c * H + h] - jm);
+                far_f[c * H + h] = f;
+                jl += f * far_l[c * H + h];
             }
-            if (G > 1) {
-                far_o[threadIdx.x] = o;
-                continue;
-            }
-            for (int c = 0; c < nc; ++c) jl += exp2_(far_m[c * C::kHeads + h] - jm) * far_l[c * C::kHeads + h];
-            finish(j, h, d, jm, jl, o.x);
-            finish(j, h, d + 1, jm, jl, o.y);
-            finish(j, h, d + 2, jm, jl, o.z);
-            finish(j, h, d + 3, jm, jl, o.w);
+            for (int o = 16; o; o >>= 1) jl += __shfl_xor_sync(~0u, jl, o);
+            if (lane == 0) joint_of[h] = make_float2(jm, jl);
         }
         __syncthreads();
-        if constexpr (G > 1) {
-            for (int e = threadIdx.x; e < C::kHeads * D; e += T) {
-                const int h = e / D, d = e % D;
-                float jm = -FLT_MAX, jl = 0.f, jo = 0.f;
-                for (int c = 0; c < nc; ++c) jm = fmaxf(jm, far_m[c * C::kHeads + h]);
-                for (int c = 0; c < nc; ++c) jl += exp2_(far_m[c * C::kHeads + h] - jm) * far_l[c * C::kHeads + h];
-#pragma unroll
-                for (int k = 0; k < G; ++k) jo += reinterpret_cast<const float *>(far_o + k * E4)[e];
-                finish(j, h, d, jm, jl, jo);
+        const int grp = G > 1 ? threadIdx.x / E4 : 0;
+#pragma unroll 1
+        for (int e = G > 1 ? threadIdx.x % E4 : threadIdx.x; e < E4; e += G > 1 ? E4 : T) {
+            const int h = 4 * e / D, d = 4 * e % D;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (grp < G) {
+#pragma unroll 4
+                for (int c = grp; c < nc; c += G) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(far_of(j.a + c, j.a) + h * DP + d));
+                    const float f = far_f[c * H + h];
+                    o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+                }
+                far_o[grp * E4 + e] = o;
             }
-            __syncthreads();
         }
+        __syncthreads();
+#pragma unroll 1
+        for (int e = threadIdx.x; e < H * D; e += T) {
+            float jo = 0.f;
+#pragma unroll
+            for (int k = 0; k < G; ++k) jo += reinterpret_cast<const float *>(far_o + k * E4)[e];
+            const float2 ml = joint_of[e / D];
+            finish(j, e / D, e % D, ml.x, ml.y, jo);
+        }
+        __syncthreads();
     }
 }
 
@@ -992,6 +1031,8 @@ cudaError_t dispatch(const AttnParams &p, cudaStream_t st, bool set)
 }
 
 }  // namespace
+
+int attn_blocks(int group) { return (group + 4 * tiles_of(group) - 1) / (4 * tiles_of(group)); }
 
 // 2 partial results for each CTA, then one for each of its warps (16 at most)
 size_t attn_part_bytes(int n_sm, int group)

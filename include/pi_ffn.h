@@ -492,7 +492,10 @@ PI_API pi_status pi_kv_read(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_t
  *   lse_dev  NULL, or n_seqs x n_heads floats
  * A sequence of length 0 gives out = 0 and lse = -infinity.  A negative length
  * counts as 0, one above width * page_size as that (both are reported).
- * Rows of the cache outside the window are not read.  The result is
+ * Rows of the cache outside the window are not read.  At most 2^30 tiles of 16
+ * positions by 16 query heads of a cached head in all, as the table's sizes
+ * have it (n_seqs * (width * page_size / 16 + 3) * n_kv_heads * ceil(query heads
+ * of a cached head / 16)).  The result is
  * deterministic for given lengths.  Calls on one handle use its scratch and
  * must not overlap; a captured graph's launches count as such calls. */
 PI_API pi_status pi_paged_attention(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_table *table,
