@@ -26,7 +26,7 @@
 namespace pi {
 namespace {
 
-constexpr int kChunk = 16;            // positions
+constexpr int kStart = 2;             // what the start of an item costs, in chunks
 constexpr int kSlots = 32;            // partial results of a CTA's warps, at most (2 for each)
 
 // FMT: the cache's format.  NB: tiles of 4 query heads that share a cached head.
@@ -36,8 +36,10 @@ struct Cfg {
     static constexpr int kRow = FMT == kI8 ? D : FMT == kI4 ? D / 2 : 2 * D;   // bytes of a cached row
     static constexpr int kScale = FMT == kI8 ? 4 : FMT == kI4 ? D / 16 : 0;    // bytes of its scales
     static constexpr int kPieces = kRow / 16;
+    // Positions of a chunk: two times 16 where rows are small, for more independent work.
+    static constexpr int kTiles = kRow <= 64 ? 2 : 1, kChunk = 16 * kTiles;
     static constexpr int kCodes = kChunk * kRow;                              // bytes of a chunk's K (or V)
-    static constexpr int kOffV = kCodes, kOffS = 2 * kCodes, kOffI = kOffS + (kScale ? 256 : 0);
+    static constexpr int kOffV = kCodes, kOffS = 2 * kCodes, kOffI = kOffS + (kScale ? 16 * kChunk : 0);
     static constexpr int kStage = kOffI + 16;
     static constexpr int kHeads = 4 * NB;                                     // query heads of an item
     static constexpr int kStep = D / 16;                                      // products of 16 along the head
@@ -46,7 +48,7 @@ struct Cfg {
     static constexpr int kPart = kHeads * (kDP + 2) * 4;                      // its bytes: o, then m and l
     static constexpr int kBuf = kHeads * (kDP + 8) * 4;                       // a warp's: queries, later its result
     // Warps of a CTA: as many as registers and three stages each allow.
-    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : NB == 2 ? 6 : 8) : NB * D == 64 ? 16 : NB * D == 128 ? 12 : 8;
+    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : NB == 2 ? 6 : 8) : NB * D == 64 && FMT != kI8 ? 16 : NB * D <= 128 ? 12 : 8;
     static constexpr int kRoom = 220 * 1024 / kWarps / 16 * 16;
     static constexpr int kStages = (kRoom - kBuf) / kStage < 8 ? (kRoom - kBuf) / kStage : 8;
     static constexpr int kRing = kStages * kStage;
@@ -154,6 +156,13 @@ __device__ __forceinline__ uint32_t hfma(uint32_t v, uint32_t a, uint32_t b)
 template <uint32_t SEL>
 __device__ __forceinline__ uint32_t bytes(uint32_t w) { return hsub(__byte_perm(w, 0x64646464u, SEL), 0x64806480u); }
 
+// The j-th of four fp16 numbers.
+__device__ __forceinline__ float half_of(uint2 v, int j)
+{
+    const uint32_t w = j < 2 ? v.x : v.y;
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    return j & 1 ? __high2float(h) : __low2float(h);
+}
 // Two numbers' 16-bit roundings, and the roundings of what is left.
 template <bool BF>
 __device__ __forceinline__ uint2 split2(float a, float b)
@@ -168,12 +177,6 @@ __device__ __forceinline__ uint2 split2(float a, float b)
     const float2 f = __half22float2(h);
     const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
     return make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l));
-}
-__device__ __forceinline__ void output(uint8_t *p, long long i, int dt, float v)
-{
-    if (dt == kF32) reinterpret_cast<float *>(p)[i] = v;
-    else if (dt == kF16) reinterpret_cast<__half *>(p)[i] = __float2half(v);
-    else reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v);
 }
 
 // Eight consecutive results from shared memory.
@@ -197,9 +200,11 @@ __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -I
 
 // Positions of one sequence that its query sees, and the chunks that hold them.
 // A sequence with none has one chunk without positions, whose result is 0.
+// (CH: positions of a chunk.)
 struct Span {
     int lo, hi, c0, c1;
 };
+template <int CH>
 __device__ __forceinline__ Span span_of(const AttnParams &p, int s, bool report)
 {
     int len = __ldg(p.len + s);
@@ -211,13 +216,13 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int s, bool report)
     Span r;
     r.hi = len;
     r.lo = p.window && len > p.window ? len - p.window : 0;
-    r.c0 = r.lo / kChunk;
-    r.c1 = max((r.hi + kChunk - 1) / kChunk, r.c0 + 1);
+    r.c0 = r.lo / CH;
+    r.c1 = max((r.hi + CH - 1) / CH, r.c0 + 1);
     return r;
 }
 
-// The work of a call in units: one for each chunk, and one before each item, for
-// its start (queries, the result).  CTA c takes the units from first(c) up to
+// The work of a call in units: one for each chunk, and kStart before each item,
+// for its start (queries, the result).  CTA c takes the units from first(c) up to
 // first(c + 1): an even share, and item by item where all items are alike and
 // the CTAs a multiple of them.
 struct Shares {
@@ -261,6 +266,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     using C = Cfg<FMT, D, NB>;
     constexpr bool BF = FMT == kBF16;
     constexpr int W = C::kWarps, S = C::kStages, T = 32 * W, KS = C::kStep, P = C::kPieces, DP = C::kDP, H = C::kHeads;
+    constexpr int R = C::kTiles, CH = C::kChunk;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int sums[W], offs[T];
     // partial results: slot 2 w of warp w's first segment (in global memory), 2 w + 1 of its last (in its buffer)
@@ -277,8 +283,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     int mine = 0;
 #pragma unroll 1
     for (int s = threadIdx.x * per; s < min(n, (int(threadIdx.x) + 1) * per); ++s) {
-        const Span r = span_of(p, s, blockIdx.x == 0);
-        mine += (r.c1 - r.c0 + 1) * items;
+        const Span r = span_of<CH>(p, s, blockIdx.x == 0);
+        mine += (r.c1 - r.c0 + kStart) * items;
     }
     int scan = mine;
 #pragma unroll
@@ -321,17 +327,17 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         at.s = b * per;
         int rest = u0 - offs[b];
         for (;;) {
-            at.span = span_of(p, at.s, false);
-            const int here = (at.span.c1 - at.span.c0 + 1) * items;
+            at.span = span_of<CH>(p, at.s, false);
+            const int here = (at.span.c1 - at.span.c0 + kStart) * items;
             if (rest < here) break;
             rest -= here;
             ++at.s;
         }
-        const int nu = at.span.c1 - at.span.c0 + 1;
+        const int nu = at.span.c1 - at.span.c0 + kStart;
         at.item = unsigned(rest) / unsigned(nu);
-        const int unit = rest - at.item * nu;   // 0: the item's start
-        if (unit == 0) --left;
-        at.c = at.span.c0 + max(unit - 1, 0);
+        const int unit = rest - at.item * nu;   // below kStart: the item's start
+        left -= max(kStart - unit, 0);
+        at.c = at.span.c0 + max(unit - kStart, 0);
     }
 
     // ---- copies of one chunk into a stage --------------------------------------
@@ -340,8 +346,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     constexpr int RI = 32 / P;            // rows of one copy instruction
     const int my_row = lane / P, my_piece = lane % P;
     const unsigned slot_bytes = p.c.slot_rows * C::kRow, scale_slot = p.c.slot_rows * C::kScale;   // 2^18 at most
-    // Pages of both halves of chunk page_c + lane of sequence page_s.
-    int page_s = -1, page_c = 0, page_a = -1, page_b = -1;
+    // Pages of the 8 positions from 8 (page_g + lane) of sequence page_s.
+    int page_s = -1, page_g = 0, my_page = -1;
     int issued = 0;
     bool first = true, from_start = at.c == at.span.c0;
     auto issue = [&](int stage) {
@@ -349,46 +355,52 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             copy_commit();
             return;
         }
-        if (at.s != page_s || unsigned(at.c - page_c) >= 32u) {
+        const int pos = at.c * CH, grp = pos / 8;
+        if (at.s != page_s || unsigned(grp - page_g) >= 32u) {
             page_s = at.s;
-            page_c = at.c;
-            const int a = (at.c + lane) * kChunk, b = a + 8;   // (below 2^30 + 2^10)
-            const int32_t *row = p.c.table + at.s * p.c.tstride;
-            page_a = a < at.span.hi && a + 8 > at.span.lo ? __ldg(row + (a >> p.c.page_shift)) : -1;
-            page_b = b < at.span.hi && b + 8 > at.span.lo ? __ldg(row + (b >> p.c.page_shift)) : -1;
+            page_g = grp;
+            const int a = pos + 8 * lane;   // (below 2^30 + 2^8)
+            my_page = a < at.span.hi && a + 8 > at.span.lo
+                          ? __ldg(p.c.table + at.s * p.c.tstride + (a >> p.c.page_shift)) : -1;
         }
-        const int pa = __shfl_sync(~0u, page_a, at.c - page_c), pb = __shfl_sync(~0u, page_b, at.c - page_c);
-        const int pos = at.c * kChunk;
         // positions seen, by bit
-        unsigned mask = 0xffffu;
-        if (pos + kChunk > at.span.hi) mask &= at.span.hi > pos ? (1u << (at.span.hi - pos)) - 1 : 0;
+        unsigned mask = CH == 32 ? ~0u : 0xffffu;
+        if (pos + CH > at.span.hi) mask = at.span.hi > pos ? (1u << (at.span.hi - pos)) - 1 : 0;
         if (pos < at.span.lo) mask &= ~((1u << (at.span.lo - pos)) - 1);
-        if ((mask & 0x00ffu) && (unsigned)pa >= (unsigned)p.c.n_pages) {
-            if (lane == 0) atomicExch(p.err, int(kDevCheck));
-            mask &= 0xff00u;
-        }
-        if ((mask & 0xff00u) && (unsigned)pb >= (unsigned)p.c.n_pages) {
-            if (lane == 0) atomicExch(p.err, int(kDevCheck));
-            mask &= 0x00ffu;
-        }
-        // first rows of the halves; a row without a position is filled with zeros (its memory is not read)
-        const int in_page = pos & (p.c.page_size - 1), in_page_b = (pos + 8) & (p.c.page_size - 1);
+        // first rows of the groups of 8; a row without a position is filled with zeros (its memory is not read)
+        long long first_row[2 * R];
         const int head = at.item / blocks_per_head * p.c.head_rows;
-        const long long ra = (mask & 0x00ffu) ? (long long)pa * p.c.page_rows + (in_page * p.c.slot_rows + head) : 0;
-        const long long rb = (mask & 0xff00u) ? (long long)pb * p.c.page_rows + (in_page_b * p.c.slot_rows + head) : 0;
+#pragma unroll
+        for (int i = 0; i < 2 * R; ++i) {
+            const int page = __shfl_sync(~0u, my_page, grp - page_g + i);
+            if (unsigned(page) >= unsigned(p.c.n_pages)) {
+                if (lane == 0 && (mask >> (8 * i) & 0xffu)) atomicExch(p.err, int(kDevCheck));
+                mask &= ~(0xffu << (8 * i));
+                first_row[i] = 0;
+            } else {
+                first_row[i] = (long long)page * p.c.page_rows + (((pos + 8 * i) & (p.c.page_size - 1)) * p.c.slot_rows + head);
+            }
+        }
         const uint32_t dst = ring_u + stage * C::kStage;
 #pragma unroll
-        for (int i = 0; i < kChunk / RI; ++i) {
+        for (int i = 0; i < CH / RI; ++i) {
             const int row = my_row + i * RI;
-            const long long off = (row < 8 ? ra : rb) * C::kRow + ((row & 7) * slot_bytes + 16 * my_piece);
+            const long long off = (RI == 16 && my_row >= 8 ? first_row[i * RI / 8 + 1] : first_row[i * RI / 8]) * C::kRow +
+                                  ((row & 7) * slot_bytes + 16 * my_piece);
             const uint32_t to = dst + 16 * place(row, my_piece);
             copy_async<16>(to, p.c.k + off, (mask >> row) & 1);
             copy_async<16>(to + C::kOffV, p.c.v + off, (mask >> row) & 1);
         }
-        if (C::kScale) {   // lanes 0-15: K of position lane, 16-31: V
-            const int key = lane & 15;
-            const uint8_t *base = (lane < 16 ? p.c.ks : p.c.vs) + (key < 8 ? ra : rb) * C::kScale + (key & 7) * scale_slot;
-            copy_async<C::kScale ? C::kScale : 4>(dst + C::kOffS + lane * 8, base, (mask >> key) & 1);
+        if (C::kScale) {   // entries: K of all positions, then V
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int entry = lane + 32 * i, key = entry % CH;
+                long long row = first_row[0];
+#pragma unroll
+                for (int j = 1; j < 2 * R; ++j) row = key / 8 == j ? first_row[j] : row;
+                const uint8_t *base = (entry < CH ? p.c.ks : p.c.vs) + row * C::kScale + (key & 7) * scale_slot;
+                copy_async<C::kScale ? C::kScale : 4>(dst + C::kOffS + entry * 8, base, (mask >> key) & 1);
+            }
         }
         copy_commit();
         // what the reader has to know
@@ -404,11 +416,11 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             return;
         }
         from_start = true;
-        if (--left <= 0) return;   // (the next item's start)
+        if ((left -= kStart) <= 0) return;   // (the next item's start)
         if (++at.item == items) {
             at.item = 0;
             ++at.s;
-            at.span = span_of(p, at.s, false);
+            at.span = span_of<CH>(p, at.s, false);
         }
         at.c = at.span.c0;
     };
@@ -436,13 +448,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     int stage = 0, put = 0;
 #pragma unroll 1
     for (int u = 1 - S; u < issued; ++u) {
-        if (u >= 0) {
-            copy_wait<S - 2>();
-            __syncwarp();
-        }
         issue(put);
         put = put + 1 == S ? 0 : put + 1;
         if (u < 0) continue;
+        __syncwarp();
         const uint32_t base = ring_u + stage * C::kStage;
         const int4 info = *reinterpret_cast<const int4 *>(ring + stage * C::kStage + C::kOffI);
         const unsigned mask = unsigned(info.x);
@@ -552,97 +561,106 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             }
             ref = kLeastRef;
         }
+        copy_wait<S - 1>();
+        __syncwarp();
         auto query = [&](int i, int b) {
             return C::kQShared ? reinterpret_cast<const uint2 *>(buf)[(i * NB + b) * 32 + lane] : q[C::kQShared ? 0 : i][C::kQShared ? 0 : b];
         };
 
-        // ---- scores of head 4 b + t at positions g and g + 8
-        float x[NB][2];
-        uint2 ks[2], vs[2];   // scales of these positions
+
+        // ---- scores of head 4 b + t at positions 16 r + g and 16 r + g + 8
+        float x[NB][2 * R];
+        uint2 ks[2 * R], vs[2 * R];   // scales of these positions
         if (C::kScale) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2 * R; ++e) {
                 if (FMT == kI8) {
                     ks[e].x = lds32(base + C::kOffS + (g + 8 * e) * 8);
-                    vs[e].x = lds32(base + C::kOffS + 128 + (g + 8 * e) * 8);
+                    vs[e].x = lds32(base + C::kOffS + 8 * CH + (g + 8 * e) * 8);
                 } else {
                     ks[e] = lds64(base + C::kOffS + (g + 8 * e) * 8);
-                    vs[e] = lds64(base + C::kOffS + 128 + (g + 8 * e) * 8);
+                    vs[e] = lds64(base + C::kOffS + 8 * CH + (g + 8 * e) * 8);
                 }
             }
         }
         if (FMT == kI4) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) x[b][0] = x[b][1] = 0.f;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < P / 2; ++i) {
-                uint32_t r[4];
-                ldm4<false>(base + 16 * place(mat_row, 2 * i + mat_piece), r);
+                for (int e = 0; e < 2 * R; ++e) x[b][e] = 0.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j = 2 * i + h;
-                    const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1], s0 = r0 >> 8, s1 = r1 >> 8;
-                    // a code n at the low end of 16 bits is the number n 2^-24, four bits further up 16 n 2^-24 (the
-                    // queries there are a 16th)
-                    const uint32_t a0[4] = {r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u};
-                    const uint32_t a1[4] = {s0 & 0x000f000fu, s1 & 0x000f000fu, s0 & 0x00f000f0u, s1 & 0x00f000f0u};
-                    const uint32_t k0 = j < 2 ? ks[0].x : ks[0].y, k1 = j < 2 ? ks[1].x : ks[1].y;
-                    const __half2 h0 = *reinterpret_cast<const __half2 *>(&k0), h1 = *reinterpret_cast<const __half2 *>(&k1);
-                    const float f0 = j & 1 ? __high2float(h0) : __low2float(h0), f1 = j & 1 ? __high2float(h1) : __low2float(h1);
+            for (int i = 0; i < P / 2; ++i)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        float c[4] = {bias[FMT == kI4 ? j : 0][b], 0.f, bias[FMT == kI4 ? j : 0][b], 0.f};
-                        mma<false>(c, a0, query(2 * j, b));
-                        mma<false>(c, a1, query(2 * j + 1, b));
-                        x[b][0] += f0 * (c[0] + c[1]);
-                        x[b][1] += f1 * (c[2] + c[3]);
+                for (int rt = 0; rt < R; ++rt) {
+                    uint32_t r[4];
+                    ldm4<false>(base + 16 * place(mat_row + 16 * rt, 2 * i + mat_piece), r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = 2 * i + h;
+                        const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1], s0 = r0 >> 8, s1 = r1 >> 8;
+                        // a code n at the low end of 16 bits is the number n 2^-24, four bits further up 16 n 2^-24 (the
+                        // queries there are a 16th)
+                        const uint32_t a0[4] = {r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u};
+                        const uint32_t a1[4] = {s0 & 0x000f000fu, s1 & 0x000f000fu, s0 & 0x00f000f0u, s1 & 0x00f000f0u};
+                        const float f0 = half_of(ks[2 * rt], j), f1 = half_of(ks[2 * rt + 1], j);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            float c[4] = {bias[FMT == kI4 ? j : 0][b], 0.f, bias[FMT == kI4 ? j : 0][b], 0.f};
+                            mma<false>(c, a0, query(2 * j, b));
+                            mma<false>(c, a1, query(2 * j + 1, b));
+                            x[b][2 * rt] += f0 * (c[0] + c[1]);
+                            x[b][2 * rt + 1] += f1 * (c[2] + c[3]);
+                        }
                     }
                 }
-            }
         } else {
-            constexpr int CH = NB == 1 ? 2 : 1;   // independent sums, where there are few products to fill the pipe with
-            float c[NB][CH][4] = {};
+            constexpr int CC = NB * R == 1 ? 2 : 1;   // independent sums, where there are few products to fill the pipe with
+            float c[NB][R][CC][4] = {};
 #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                if (FMT == kI8) {
-                    if (i & 1) continue;
-                    uint32_t r[4];
-                    ldm4<false>(base + 16 * place(mat_row, i + mat_piece), r);
+            for (int i = 0; i < KS; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] ^= 0x80808080u;
-                    const uint32_t a0[4] = {bytes<0x4140>(r[0]), bytes<0x4140>(r[1]), bytes<0x4342>(r[0]), bytes<0x4342>(r[1])};
-                    const uint32_t a1[4] = {bytes<0x4140>(r[2]), bytes<0x4140>(r[3]), bytes<0x4342>(r[2]), bytes<0x4342>(r[3])};
+                for (int rt = 0; rt < R; ++rt) {
+                    if (FMT == kI8) {
+                        if (i & 1) continue;
+                        uint32_t r[4];
+                        ldm4<false>(base + 16 * place(mat_row + 16 * rt, i + mat_piece), r);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        mma<false>(c[b][0], a0, query(i, b));
-                        mma<false>(c[b][CH - 1], a1, query(i + 1 < KS ? i + 1 : i, b));
+                        for (int e = 0; e < 4; ++e) r[e] ^= 0x80808080u;
+                        const uint32_t a0[4] = {bytes<0x4140>(r[0]), bytes<0x4140>(r[1]), bytes<0x4342>(r[0]), bytes<0x4342>(r[1])};
+                        const uint32_t a1[4] = {bytes<0x4140>(r[2]), bytes<0x4140>(r[3]), bytes<0x4342>(r[2]), bytes<0x4342>(r[3])};
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            mma<false>(c[b][rt][0], a0, query(i, b));
+                            mma<false>(c[b][rt][CC - 1], a1, query(i + 1 < KS ? i + 1 : i, b));
+                        }
+                    } else {
+                        uint32_t r[4];
+                        ldm4<false>(base + 16 * place(mat_row + 16 * rt, 2 * i + mat_piece), r);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) mma<BF>(c[b][rt][i % CC], r, query(i, b));
                     }
-                } else {
-                    uint32_t r[4];
-                    ldm4<false>(base + 16 * place(mat_row, 2 * i + mat_piece), r);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) mma<BF>(c[b][i % CH], r, query(i, b));
                 }
-            }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if (CH == 2) {
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) c[b][0][e] += c[b][CH - 1][e];
+                for (int rt = 0; rt < R; ++rt) {
+                    float (&y)[4] = c[b][rt][0];
+                    if (CC == 2) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] += c[b][rt][CC - 1][e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[b][2 * rt + e] = C::kF ? whole(y[2 * e], y[2 * e + 1]) : y[2 * e] + y[2 * e + 1];
+                        if (FMT == kI8) x[b][2 * rt + e] *= __uint_as_float(ks[2 * rt + e].x);
+                    }
                 }
-                x[b][0] = C::kF ? whole(c[b][0][0], c[b][0][1]) : c[b][0][0] + c[b][0][1];
-                x[b][1] = C::kF ? whole(c[b][0][2], c[b][0][3]) : c[b][0][2] + c[b][0][3];
-                if (FMT == kI8) {
-                    x[b][0] *= __uint_as_float(ks[0].x);
-                    x[b][1] *= __uint_as_float(ks[1].x);
-                }
-            }
         }
         bool grows = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2 * R; ++e) {
                 float &y = x[b][e];
                 y *= factor[b];
                 if (p.softcap > 0.f) {   // cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap))
@@ -654,11 +672,17 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             }
         int big = 0;   // exponent of the largest V scale
         if (FMT == kI8) {
-            big = __float_as_int(fmaxf(__uint_as_float(vs[0].x), __uint_as_float(vs[1].x))) >> 23;
+            float v = __uint_as_float(vs[0].x);
+#pragma unroll
+            for (int e = 1; e < 2 * R; ++e) v = fmaxf(v, __uint_as_float(vs[e].x));
+            big = __float_as_int(v) >> 23;
         } else if (FMT == kI4) {
-            __half2 hm = __hmax2(*reinterpret_cast<const __half2 *>(&vs[0].x), *reinterpret_cast<const __half2 *>(&vs[1].x));
-            if (D == 128)
-                hm = __hmax2(hm, __hmax2(*reinterpret_cast<const __half2 *>(&vs[0].y), *reinterpret_cast<const __half2 *>(&vs[1].y)));
+            __half2 hm = *reinterpret_cast<const __half2 *>(&vs[0].x);
+#pragma unroll
+            for (int e = 0; e < 2 * R; ++e) {
+                hm = __hmax2(hm, *reinterpret_cast<const __half2 *>(&vs[e].x));
+                if (D == 128) hm = __hmax2(hm, *reinterpret_cast<const __half2 *>(&vs[e].y));
+            }
             big = __float_as_int(__half2float(__hmax(__low2half(hm), __high2half(hm)))) >> 23;
         }
         if (__any_sync(~0u, grows || (C::kScale && big > ref))) {
@@ -667,12 +691,11 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                 if (FMT == kI4 && big == 255) {   // an infinite scale spoils its own group only: the largest of the others
                     big = 0;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2 * R; ++e)
 #pragma unroll
-                        for (int i = 0; i < D / 64; ++i) {
-                            const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(i ? &vs[e].y : &vs[e].x));
-                            if (sc.x < INFINITY) big = max(big, __float_as_int(sc.x) >> 23);
-                            if (sc.y < INFINITY) big = max(big, __float_as_int(sc.y) >> 23);
+                        for (int j = 0; j < D / 32; ++j) {
+                            const float sc = half_of(vs[e], j);
+                            if (sc < INFINITY) big = max(big, __float_as_int(sc) >> 23);
                         }
                 }
                 const int grown = min(int(__reduce_max_sync(~0u, unsigned(max(ref, big)))), 253);
@@ -681,7 +704,9 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float top = fmaxf(m[b], fmaxf(x[b][0], x[b][1]));
+                float top = m[b];
+#pragma unroll
+                for (int e = 0; e < 2 * R; ++e) top = fmaxf(top, x[b][e]);
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
@@ -701,7 +726,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2 * R; ++e) {
                 // F16: weights carry a factor 2^14, so that the low parts of small ones stay normal numbers
                 x[b][e] = exp2_(FMT == kF16 ? x[b][e] - m[b] + 14.f : x[b][e] - m[b]);
                 l[b] += x[b][e];
@@ -710,67 +735,71 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         const float f = pow2_of(254 - ref) * 0x1p13f;
         if (FMT == kI4) {
 #pragma unroll
-            for (int i = 0; i < P / 2; ++i) {
-                uint32_t r[4];
-                ldm4<true>(base + C::kOffV + 16 * place(mat_row, 2 * i + mat_piece), r);
+            for (int i = 0; i < P / 2; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j = 2 * i + h;
-                    // element 4 g + e of positions 2t, 2t + 1 at bits 4 e: under the exponent of 1024 a code is 1024 + n
-                    // or 1024 + 16 n; less 8 these are exact
-                    uint32_t a[2][4];
+                for (int rt = 0; rt < R; ++rt) {
+                    uint32_t r[4];
+                    ldm4<true>(base + C::kOffV + 16 * place(mat_row + 16 * rt, 2 * i + mat_piece), r);
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        const uint32_t w = r[2 * h + o], z = w >> 8;
-                        a[0][2 * o] = hsub((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        a[0][2 * o + 1] = hfma((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
-                        a[1][2 * o] = hsub((z & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        a[1][2 * o + 1] = hfma((z & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
-                    }
-                    const uint32_t k0 = j < 2 ? vs[0].x : vs[0].y, k1 = j < 2 ? vs[1].x : vs[1].y;
-                    const __half2 h0 = *reinterpret_cast<const __half2 *>(&k0), h1 = *reinterpret_cast<const __half2 *>(&k1);
-                    const float f0 = f * (j & 1 ? __high2float(h0) : __low2float(h0));
-                    const float f1 = f * (j & 1 ? __high2float(h1) : __low2float(h1));
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = 2 * i + h;
+                        // element 4 g + e of positions 2t, 2t + 1 at bits 4 e: under the exponent of 1024 a code is 1024 + n
+                        // or 1024 + 16 n; less 8 these are exact
+                        uint32_t a[2][4];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint2 w = make_uint2(transpose8(split<false>(x[b][0] * f0)), transpose8(split<false>(x[b][1] * f1)));
-                        mma<false>(acc[b][2 * j], a[0], w);
-                        mma<false>(acc[b][2 * j + 1], a[1], w);
+                        for (int o = 0; o < 2; ++o) {
+                            const uint32_t w = r[2 * h + o], z = w >> 8;
+                            a[0][2 * o] = hsub((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                            a[0][2 * o + 1] = hfma((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+                            a[1][2 * o] = hsub((z & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                            a[1][2 * o + 1] = hfma((z & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+                        }
+                        const float f0 = f * half_of(vs[2 * rt], j), f1 = f * half_of(vs[2 * rt + 1], j);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const uint2 w = make_uint2(transpose8(split<false>(x[b][2 * rt] * f0)),
+                                                       transpose8(split<false>(x[b][2 * rt + 1] * f1)));
+                            mma<false>(acc[b][2 * j], a[0], w);
+                            mma<false>(acc[b][2 * j + 1], a[1], w);
+                        }
                     }
                 }
-            }
         } else {
-            uint2 w[NB];
+            uint2 w[NB][R];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if (FMT == kI8) {
-                    x[b][0] *= __uint_as_float(vs[0].x) * f;
-                    x[b][1] *= __uint_as_float(vs[1].x) * f;
-                }
-                w[b] = make_uint2(transpose8(split<BF>(x[b][0])), transpose8(split<BF>(x[b][1])));
-            }
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                uint32_t r[4];
-                if (FMT == kI8) {
-                    if (i & 1) continue;
-                    ldm4<true>(base + C::kOffV + 16 * place(mat_row_v, i + mat_piece_v), r);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] ^= 0x80808080u;
-                    // elements 2g and 2g + 1 of positions 2t, 2t + 1 in turn
-                    const uint32_t a0[4] = {bytes<0x4240>(r[0]), bytes<0x4341>(r[0]), bytes<0x4240>(r[1]), bytes<0x4341>(r[1])};
-                    const uint32_t a1[4] = {bytes<0x4240>(r[2]), bytes<0x4341>(r[2]), bytes<0x4240>(r[3]), bytes<0x4341>(r[3])};
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        mma<false>(acc[b][i], a0, w[b]);
-                        mma<false>(acc[b][i + 1 < KS ? i + 1 : i], a1, w[b]);
+                for (int rt = 0; rt < R; ++rt) {
+                    if (FMT == kI8) {
+                        x[b][2 * rt] *= __uint_as_float(vs[2 * rt].x) * f;
+                        x[b][2 * rt + 1] *= __uint_as_float(vs[2 * rt + 1].x) * f;
                     }
-                } else {
-                    ldm4<true>(base + C::kOffV + 16 * place(mat_row_v, 2 * i + mat_piece_v), r);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) mma<BF>(acc[b][i], r, w[b]);
+                    w[b][rt] = make_uint2(transpose8(split<BF>(x[b][2 * rt])), transpose8(split<BF>(x[b][2 * rt + 1])));
                 }
-            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) {
+                    uint32_t r[4];
+                    if (FMT == kI8) {
+                        if (i & 1) continue;
+                        ldm4<true>(base + C::kOffV + 16 * place(mat_row_v + 16 * rt, i + mat_piece_v), r);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) r[e] ^= 0x80808080u;
+                        // elements 2g and 2g + 1 of positions 2t, 2t + 1 in turn
+                        const uint32_t a0[4] = {bytes<0x4240>(r[0]), bytes<0x4341>(r[0]), bytes<0x4240>(r[1]), bytes<0x4341>(r[1])};
+                        const uint32_t a1[4] = {bytes<0x4240>(r[2]), bytes<0x4341>(r[2]), bytes<0x4240>(r[3]), bytes<0x4341>(r[3])};
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            mma<false>(acc[b][i], a0, w[b][rt]);
+                            mma<false>(acc[b][i + 1 < KS ? i + 1 : i], a1, w[b][rt]);
+                        }
+                    } else {
+                        ldm4<true>(base + C::kOffV + 16 * place(mat_row_v + 16 * rt, 2 * i + mat_piece_v), r);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) mma<BF>(acc[b][i], r, w[b][rt]);
+                    }
+                }
         }
 
         if (info.y & kLast) {   // o to the buffer, one row for each head
@@ -818,8 +847,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         *reinterpret_cast<float4 *>(warp_part + e) = *reinterpret_cast<const float4 *>(buf + e);
                 }
             }
-            __syncwarp();
         }
+        __syncwarp();   // all have read the stage: the next copy may take it
         stage = stage + 1 == S ? 0 : stage + 1;
     }
     copy_wait<0>();
@@ -841,14 +870,14 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             j.slots = valid & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : ~0u);
             int start = offs[s / per];
             for (int r = s / per * per; r < s; ++r) {
-                const Span sp = span_of(p, r, false);
-                start += (sp.c1 - sp.c0 + 1) * items;
+                const Span sp = span_of<CH>(p, r, false);
+                start += (sp.c1 - sp.c0 + kStart) * items;
             }
-            const Span sp = span_of(p, s, false);
+            const Span sp = span_of<CH>(p, s, false);
             const int nc = sp.c1 - sp.c0;
-            start += item * (nc + 1);
-            j.a = shares.of(start + 1);   // CTAs of its first and last chunk
-            j.b = shares.of(start + nc);
+            start += item * (nc + kStart) + kStart;
+            j.a = shares.of(start);   // CTAs of its first and last chunk
+            j.b = shares.of(start + nc - 1);
         }
         if (lane == 0) n_joints = __popc(heads);
     }
@@ -861,12 +890,23 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     // this CTA's partial results of items that others share: 2 CTA for one that began before it, 2 CTA + 1 for one
     // that begins in it
     auto far_of = [&](int cta, int a) { return p.part + (size_t)(2 * cta + (cta == a)) * (C::kPart / 4); };
-    // an item's results leave with o as it is, or divided by l
-    auto finish = [&](const Joint &j, int h, int d, float jm, float jl, float jo) {
+    // four results of an item
+    auto finish = [&](const Joint &j, int h, int d, float jm, float jl, float4 o) {
         const int hb = j.item % blocks_per_head * H + h;
         if (hb >= p.group) return;
         const int head = j.item / blocks_per_head * p.group + hb;
-        output(p.out, j.s * p.os + (long long)head * D + d, p.dt, jl == 0.f ? 0.f : jo / jl);
+        const long long at4 = j.s * p.os + (long long)head * D + d;
+        const float unit = jl == 0.f ? 0.f : 1.f / jl;
+        o.x *= unit, o.y *= unit, o.z *= unit, o.w *= unit;
+        if (p.dt == kF32) {
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + at4) = o;
+        } else if (p.dt == kF16) {
+            const __half2 v[2] = {__floats2half2_rn(o.x, o.y), __floats2half2_rn(o.z, o.w)};
+            *reinterpret_cast<uint2 *>(p.out + 2 * at4) = *reinterpret_cast<const uint2 *>(v);
+        } else {
+            const __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
+            *reinterpret_cast<uint2 *>(p.out + 2 * at4) = *reinterpret_cast<const uint2 *>(v);
+        }
         if (p.lse && d == 0) p.lse[(long long)j.s * p.heads + head] = lse_of(jm, jl);
     };
     // weights of the slots by (item, head) in place of their m; the sums m and l in the rings, which are empty
@@ -889,30 +929,34 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     }
     __syncthreads();
 #pragma unroll 1
-    for (int e = threadIdx.x; e < nj * H * D; e += T) {
-        const Joint &j = joints[e / (H * D)];
-        const int h = e / D % H, d = e % D, first_slot = __ffs(j.slots) - 1;
-        float jo = 0.f;
+    for (int e = threadIdx.x; e < nj * H * D / 4; e += T) {
+        const Joint &j = joints[e / (H * D / 4)];
+        const int h = e / (D / 4) % H, d = 4 * e % D, first_slot = __ffs(j.slots) - 1;
+        float4 jo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (unsigned k = j.slots; k;) {   // four slots at a time
-            float v[4], f[4];
+            float4 v[4];
+            float f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int slot = k ? __ffs(k) - 1 : first_slot;
-                v[i] = part_of(slot)[h * DP + d];
+                v[i] = *reinterpret_cast<const float4 *>(part_of(slot) + h * DP + d);
                 f[i] = part_m[slot][h];
-                if (!k) v[i] = f[i] = 0.f;
+                if (!k) {
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    f[i] = 0.f;
+                }
                 k &= k - 1;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) jo += f[i] * v[i];
+            for (int i = 0; i < 4; ++i) jo.x += f[i] * v[i].x, jo.y += f[i] * v[i].y, jo.z += f[i] * v[i].z, jo.w += f[i] * v[i].w;
         }
-        const float jm = joint_m[e / D], jl = joint_l[e / D];
+        const float jm = joint_m[e / (D / 4)], jl = joint_l[e / (D / 4)];
         if (j.a == j.b) {
             finish(j, h, d, jm, jl, jo);
         } else {
             float *dst = far_of(blockIdx.x, j.a);
-            dst[h * DP + d] = jo;
+            *reinterpret_cast<float4 *>(dst + h * DP + d) = jo;
             if (d == 0) {
                 dst[H * DP + h] = jm;
                 dst[H * (DP + 1) + h] = jl;
@@ -980,12 +1024,15 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         }
         __syncthreads();
 #pragma unroll 1
-        for (int e = threadIdx.x; e < H * D; e += T) {
-            float jo = 0.f;
+        for (int e = threadIdx.x; e < E4; e += T) {
+            float4 jo = far_o[e];
 #pragma unroll
-            for (int k = 0; k < G; ++k) jo += reinterpret_cast<const float *>(far_o + k * E4)[e];
-            const float2 ml = joint_of[e / D];
-            finish(j, e / D, e % D, ml.x, ml.y, jo);
+            for (int k = 1; k < G; ++k) {
+                const float4 v = far_o[k * E4 + e];
+                jo.x += v.x, jo.y += v.y, jo.z += v.z, jo.w += v.w;
+            }
+            const float2 ml = joint_of[4 * e / D];
+            finish(j, 4 * e / D, 4 * e % D, ml.x, ml.y, jo);
         }
         __syncthreads();
     }
