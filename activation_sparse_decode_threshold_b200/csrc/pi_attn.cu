@@ -106,7 +106,7 @@ pi_status check_rows(const char *name, const void *p, long long &stride, int len
 }  // namespace
 
 struct pi_int4 {
-    int n = 0, k = 0, ku = 0, device = 0, n_sm = 0;
+    int n = 0, k = 0, ku = 0, device = 0, n_sm = 0, clusters[3] = {0, 0, 0};
     uint8_t *w = nullptr;
 };
 
@@ -148,6 +148,7 @@ pi_status pi_int4_create(int n_rows, int n_cols, const void *q_dev, const void *
     const size_t bytes = size_t((n_rows + 15) / 16) * m->ku * pi::kInt4Unit;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e = pi::int4_setup();
+    if (e == cudaSuccess) e = pi::int4_clusters(m->clusters);
     if (e == cudaSuccess) e = cudaMalloc(&m->w, bytes);
     if (e == cudaSuccess)
         e = pi::int4_pack(static_cast<const uint8_t *>(q_dev), static_cast<const uint16_t *>(s_dev), m->w, n_rows, n_cols,
@@ -208,6 +209,7 @@ pi_status pi_int4_matvec(pi_int4_t m, int n_tokens, pi_dtype x_dtype, const void
     p.ys = ys;
     p.eps = norm_eps;
     p.n_sm = m->n_sm;
+    for (int i = 0; i < 3; ++i) p.clusters[i] = m->clusters[i];
     PI_CUDA(pi::int4_matvec(p, static_cast<cudaStream_t>(stream)), "pi_int4_matvec");
     return PI_OK;
 }

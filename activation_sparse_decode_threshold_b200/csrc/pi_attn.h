@@ -23,8 +23,9 @@ struct Int4Params {
     uint8_t *y;
     long long xs, ys;       // elements between tokens
     float eps;              // 0: no norm
-    int n_sm;
+    int n_sm, clusters[3];  // SMs; clusters of 2, 4, 8 CTAs that run at once
 };
+cudaError_t int4_clusters(int (&clusters)[3]);
 cudaError_t int4_pack(const uint8_t *q, const uint16_t *s, uint8_t *dst, int n, int k, cudaStream_t st);
 cudaError_t int4_setup();   // once per device, before any launch
 cudaError_t int4_matvec(const Int4Params &p, cudaStream_t st);

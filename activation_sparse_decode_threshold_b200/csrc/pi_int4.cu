@@ -13,9 +13,9 @@
 namespace pi {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreadsMv = 32 * kWarps;
-constexpr int kXBytes = 112 * 1024;    // shared memory for a chunk of x: 512 columns of 96 parts at least
+constexpr int kXBytes = 104 * 1024;    // shared memory for a chunk of x: 512 columns of 96 parts at least
+constexpr int kMaxCluster = 8;
+constexpr int kShareX = 64 * 1024;     // a CTA's part of x above this: the columns are split over more CTAs
 
 // Unit (row tile, 64 columns): lane (g = lane / 4, t = lane % 4) finds at 16 lane
 // the eight columns 8t .. 8t+7 of rows g and g + 8, first of the unit's first
@@ -100,6 +100,34 @@ __device__ __forceinline__ void load8(const uint8_t *x, long long i, int xt, flo
     }
 }
 
+// The matrix is read once: past L1, and first to leave L2.
+__device__ __forceinline__ uint4 ldg_stream(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ldg_stream(const uint2 *p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A number in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float peer(const float *p, int rank)
+{
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // Parts of x: F16 and BF16 are their own 16-bit numbers; an F32 is three bf16
 // numbers, each the leading 8 bits of what is left (cut off, so that no part
 // overflows; 24 bits in all).  An infinity or NaN stays in the first part.
@@ -112,130 +140,257 @@ __device__ __forceinline__ float value_of(const uint8_t *p, long long i, int dt)
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-// One CTA per tile of 16 rows; the warps share the columns of each chunk of x.
+// A product's shape in shared memory.  W: warps of a CTA.
+template <int NT>
+struct MvCfg {
+    static constexpr int kWarps = NT <= 4 ? 16 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kAhead = 4;                                // units in flight for each warp
+    static constexpr int kSlot = 16 * 8 * NT;                       // sums of a warp for one row tile
+    static constexpr int kSums = kWarps * 16 * kInt4MaxTokens;      // of a CTA's row tiles: [tile][token][row]
+    static constexpr int kFixed = (2 * kWarps * kSlot + kSums) * 4; // bytes before the chunk of x
+};
+
+// A cluster takes row tiles (of 16), up to kWarps at a time; its CTAs share the
+// columns.  A CTA's part, tiles x units of 64 columns, is laid end to end and
+// shared out evenly over its warps, so that a warp has parts of two tiles at
+// most: the sums of these go to two slots in shared memory, from there in order
+// to the tile's sums, and from the CTAs, in order, to y.  Bound by the matrix's
+// bytes: each warp keeps kAhead units of 576 bytes under way in registers, and x
+// is brought to each CTA once (for 13 tokens of 8192 columns it is 213 KB, more
+// than the CTA's share of the matrix: hence the clusters).
 // PARTS: 3 for F32 x, else 1.  NT: tiles of 8 columns of B (tokens * PARTS).
 template <bool BF, int PARTS, int NT>
-__global__ void __launch_bounds__(kThreadsMv) k_matvec(Int4Params p, int chunk)
+__global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p, int log_cs, int clusters, int chunk)
 {
+    using C = MvCfg<NT>;
+    constexpr int W = C::kWarps, T = C::kThreads, U = C::kAhead;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float ssq[kInt4MaxTokens][kWarps];
-    uint16_t *xs = reinterpret_cast<uint16_t *>(smem);
+    __shared__ float ssq[kInt4MaxTokens * W];
+    __shared__ float total_sq[kInt4MaxTokens];
+    __shared__ int from_warp[W], to_warp[W];   // of a tile: the slot of its first warp, its last warp
+    float *slots = reinterpret_cast<float *>(smem), *sums = slots + 2 * W * C::kSlot;
+    uint16_t *xs = reinterpret_cast<uint16_t *>(smem + C::kFixed);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
-    const int cols = p.tokens * PARTS;
-    const int stride = chunk + 32;   // 64 bytes past a multiple of 128: no bank conflicts
-    const long long tile = blockIdx.x;
-    float acc[NT][4] = {};
-    if (p.eps > 0.f) {
-        for (int t = 0; t < p.tokens; ++t) {
-            float ss = 0.f;
-            for (int i = threadIdx.x * 8; i < p.k; i += kThreadsMv * 8) {
-                float v[8];
-                load8(p.x, t * p.xs + i, p.xt, v);
+    const int cols = p.tokens * PARTS, stride = chunk * 64 + 32;   // 64 bytes past a multiple of 128: no bank conflicts
+    const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1), cluster = blockIdx.x >> log_cs;
+    const int tiles = (p.n + 15) / 16;
+    const unsigned each = unsigned(tiles) / unsigned(clusters), more = tiles - each * clusters;
+    const int t_begin = cluster * each + min(unsigned(cluster), more), t_end = t_begin + each + (unsigned(cluster) < more);
+    const int k_begin = p.ku * rank >> log_cs, k_end = p.ku * (rank + 1) >> log_cs;   // units
+    const bool one_pass = k_end - k_begin <= chunk;
+
+    for (int t0 = t_begin; t0 < t_end; t0 += W) {
+        const int nt = min(W, t_end - t0);
+        for (int k0 = k_begin; k0 < k_end; k0 += chunk) {
+            const int ks = min(chunk, k_end - k0);
+            const int busy = min(W, nt * ks), share = unsigned(nt * ks) / unsigned(busy), rest = nt * ks - share * busy;
+            const int first = min(warp, busy) * share + min(warp, rest), end = first + (warp < busy ? share + (warp < rest) : 0);
+            // the first units are under way before x is
+            const int tile = first / ks;
+            int k = first - tile * ks;
+            const uint8_t *next = p.w + ((long long)(t0 + tile) * p.ku + k0 + k) * kInt4Unit;
+            const long long jump = (long long)(p.ku - ks) * kInt4Unit;
+            int next_k = k, ahead = first;
+            uint4 wq[U];
+            uint2 ws[U];
+            auto load = [&](int i) {
+                if (ahead >= end) return;
+                wq[i] = ldg_stream(reinterpret_cast<const uint4 *>(next + 16 * lane));
+                ws[i] = ldg_stream(reinterpret_cast<const uint2 *>(next + 512 + 8 * g));
+                ++ahead;
+                next += kInt4Unit;
+                if (++next_k == ks) {
+                    next_k = 0;
+                    next += jump;
+                }
+            };
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+            for (int i = 0; i < U; ++i) load(i);
+            // a tile belongs to the warps from the one with its first unit on
+            if (lane == 0 && first < end) {
+                const int last = (end - 1 - first + k) / ks;   // 1: the warp goes on into a second tile
+                if (k == 0) from_warp[tile] = 2 * warp;
+                if (last) from_warp[tile + 1] = 2 * warp + 1;
+                if (first + ks - k <= end) to_warp[tile] = warp;
+                if (last && first + 2 * ks - k <= end) to_warp[tile + 1] = warp;
             }
-            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-            if (lane == 0) ssq[t][warp] = ss;
-        }
-    }
-    for (int k0 = 0; k0 < p.ku * 64; k0 += chunk) {
-        const int here = min(chunk, p.ku * 64 - k0);
-        __syncthreads();
-        for (int i = threadIdx.x; i < p.tokens * (here / 8); i += kThreadsMv) {
-            const int t = i / (here / 8), at = i % (here / 8) * 8;
-            uint16_t *dst = xs + t * stride + at;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (PARTS == 1) {
-                if (k0 + at < p.k) w = *reinterpret_cast<const uint4 *>(p.x + 2 * (t * p.xs + k0 + at));
-                *reinterpret_cast<uint4 *>(dst) = w;
-            } else {
-                float v[8] = {};
-                if (k0 + at < p.k) load8(p.x, t * p.xs + k0 + at, p.xt, v);
+            if (t0 == t_begin || !one_pass) {
+                const int pieces = ks * 8;   // of 8 columns
+#pragma unroll 2
+                for (int i = threadIdx.x; i < p.tokens * pieces; i += T) {
+                    const int t = i / pieces, at = (i - t * pieces) * 8, col = k0 * 64 + at;
+                    uint16_t *dst = xs + t * stride + at;
+                    if (PARTS == 1) {
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (col < p.k) w = *reinterpret_cast<const uint4 *>(p.x + 2 * (t * p.xs + col));
+                        *reinterpret_cast<uint4 *>(dst) = w;
+                    } else {
+                        float v[8] = {};
+                        if (col < p.k) load8(p.x, t * p.xs + col, p.xt, v);
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    uint32_t u[4];
+                        for (int part = 0; part < PARTS; ++part) {
+                            uint32_t u[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float c = cut(v[e]);
-                        const uint32_t b = isnan(v[e]) ? 0x7fc0u : __float_as_uint(v[e]) >> 16;
-                        u[e / 2] = e & 1 ? u[e / 2] | (b << 16) : b;
-                        v[e] = isfinite(v[e]) ? v[e] - c : 0.f;
+                            for (int e = 0; e < 8; ++e) {
+                                const float c = cut(v[e]);
+                                const uint32_t b = isnan(v[e]) ? 0x7fc0u : __float_as_uint(v[e]) >> 16;
+                                u[e / 2] = e & 1 ? u[e / 2] | (b << 16) : b;
+                                v[e] = isfinite(v[e]) ? v[e] - c : 0.f;
+                            }
+                            *reinterpret_cast<uint4 *>(dst + part * p.tokens * stride) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(dst + part * p.tokens * stride) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                if (p.eps > 0.f && t0 == t_begin) {
+                    // sums of squares: one warp for each token, or for each of several pieces of it
+                    const int split = max(1, W / p.tokens);
+                    for (int i = warp; i < p.tokens * split; i += W) {
+                        const int t = i / split, piece = i - t * split;
+                        float ss = 0.f;
+#pragma unroll 2
+                        for (int c = piece * 32 + lane; c < pieces; c += 32 * split) {
+                            const int col = k0 * 64 + 8 * c;
+                            if (col >= p.k) break;
+                            float v[8];
+                            load8(p.x, t * p.xs + col, p.xt, v);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+                        }
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                        if (lane == 0) ssq[i] = ss;
+                    }
+                }
+                __syncthreads();
+                if (p.eps > 0.f && t0 == t_begin && threadIdx.x < p.tokens) {
+                    const int split = max(1, W / p.tokens);
+                    float ss = k0 == k_begin ? 0.f : total_sq[threadIdx.x];
+                    for (int i = 0; i < split; ++i) ss += ssq[threadIdx.x * split + i];
+                    total_sq[threadIdx.x] = ss;
                 }
             }
-        }
-        __syncthreads();
-        for (int u = warp; u < here / 64; u += kWarps) {
-            const uint8_t *w = p.w + (tile * p.ku + k0 / 64 + u) * kInt4Unit;
-            const uint4 q = *reinterpret_cast<const uint4 *>(w + 16 * lane);
-            const uint2 s = *reinterpret_cast<const uint2 *>(w + 512 + 8 * g);
-            const uint32_t qq[4] = {q.x, q.y, q.z, q.w}, sp[2] = {s.x, s.y};
+
+            // ---- the warp's units
+            float acc[NT][4] = {};
+            float *slot = slots + 2 * warp * C::kSlot;
+            auto flush = [&]() {
 #pragma unroll
-            for (int grp = 0; grp < 2; ++grp) {
-                uint32_t lo[4], hi[4];
-                nibbles<BF>(qq[2 * grp], lo);
-                nibbles<BF>(qq[2 * grp + 1], hi);
-                const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&sp[grp]));
+                for (int nt2 = 0; nt2 < NT; ++nt2) {
+                    *reinterpret_cast<float2 *>(slot + g * 8 * NT + nt2 * 8 + 2 * t4) = make_float2(acc[nt2][0], acc[nt2][1]);
+                    *reinterpret_cast<float2 *>(slot + (g + 8) * 8 * NT + nt2 * 8 + 2 * t4) = make_float2(acc[nt2][2], acc[nt2][3]);
+                    acc[nt2][0] = acc[nt2][1] = acc[nt2][2] = acc[nt2][3] = 0.f;
+                }
+                slot += C::kSlot;
+            };
+            for (int u = first; u < end;) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int col = min(nt * 8 + g, cols - 1);
-                    const uint4 b = *reinterpret_cast<const uint4 *>(xs + col * stride + u * 64 + grp * 32 + t4 * 8);
-                    float c[4] = {};
-                    mma16816<BF>(c, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                    mma16816<BF>(c, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-                    acc[nt][0] += sc.x * c[0];
-                    acc[nt][1] += sc.x * c[1];
-                    acc[nt][2] += sc.y * c[2];
-                    acc[nt][3] += sc.y * c[3];
+                for (int i = 0; i < U; ++i) {
+                    if (u >= end) break;
+                    const uint32_t qq[4] = {wq[i].x, wq[i].y, wq[i].z, wq[i].w}, sp[2] = {ws[i].x, ws[i].y};
+                    load(i);
+#pragma unroll
+                    for (int grp = 0; grp < 2; ++grp) {
+                        uint32_t lo[4], hi[4];
+                        nibbles<BF>(qq[2 * grp], lo);
+                        nibbles<BF>(qq[2 * grp + 1], hi);
+                        const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&sp[grp]));
+#pragma unroll
+                        for (int n8 = 0; n8 < NT; ++n8) {
+                            const int col = min(n8 * 8 + g, cols - 1);
+                            const uint4 b = *reinterpret_cast<const uint4 *>(xs + col * stride + k * 64 + grp * 32 + t4 * 8);
+                            float c[4] = {};
+                            mma16816<BF>(c, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                            mma16816<BF>(c, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                            acc[n8][0] += sc.x * c[0];
+                            acc[n8][1] += sc.x * c[1];
+                            acc[n8][2] += sc.y * c[2];
+                            acc[n8][3] += sc.y * c[3];
+                        }
+                    }
+                    ++u;
+                    if (++k == ks) {
+                        k = 0;
+                        flush();
+                    }
                 }
             }
-        }
-    }
-    __syncthreads();
-    // sums of the warps, in order
-    float *red = reinterpret_cast<float *>(smem);   // [warp][16 rows][8 NT]
+            if (k != 0 && first < end) flush();
+            __syncthreads();
+            // ---- the tiles' sums: warps in order, parts from the least
+            for (int i = threadIdx.x; i < nt * 16 * p.tokens; i += T) {
+                const int r = i % 16, j = i / 16 % nt, t = i / 16 / nt;
+                float y = k0 == k_begin ? 0.f : sums[(j * p.tokens + t) * 16 + r];
+                const int s0 = from_warp[j], s1 = 2 * to_warp[j];
+                const float *src = slots + s0 * C::kSlot + r * 8 * NT + t;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+                for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
+                src = slots + (s0 / 2 + 1) * 2 * C::kSlot + r * 8 * NT + t;
+#pragma unroll 4
+                for (int w = s0 / 2 + 1; w <= s1 / 2; ++w, src += 2 * C::kSlot) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            red[(warp * 16 + g + 8 * (e >> 1)) * (8 * NT) + nt * 8 + 2 * t4 + (e & 1)] = acc[nt][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * p.tokens; i += kThreadsMv) {
-        const int r = i % 16, t = i / 16;
-        const long long row = tile * 16 + r;
-        if (row >= p.n) continue;
-        float y = 0.f;
-        for (int part = PARTS - 1; part >= 0; --part)
-            for (int w = 0; w < kWarps; ++w) y += red[(w * 16 + r) * (8 * NT) + part * p.tokens + t];
-        if (p.eps > 0.f) {
-            float ss = 0.f;
-            for (int w = 0; w < kWarps; ++w) ss += ssq[t][w];
-            y *= 1.f / sqrtf(ss / float(p.k) + p.eps);
+                    for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
+                }
+                sums[(j * p.tokens + t) * 16 + r] = y;
+            }
+            if (cs == 1 || k0 + chunk < k_end) __syncthreads();
         }
-        const long long at = t * p.ys + row;
-        if (p.add) y += value_of(p.add, at, p.yt);
-        if (p.yt == kF32) reinterpret_cast<float *>(p.y)[at] = y;
-        else if (p.yt == kF16) reinterpret_cast<__half *>(p.y)[at] = __float2half(y);
-        else reinterpret_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16(y);
+        // ---- over the cluster's CTAs, in order, to y
+        if (cs > 1) cluster_sync();
+        const int all = nt * 16 * p.tokens;
+        for (int i = (all * rank >> log_cs) + threadIdx.x; i < all * (rank + 1) >> log_cs; i += T) {
+            const int r = i % 16, t = i / 16 % p.tokens, j = i / 16 / p.tokens;
+            const long long row = (long long)(t0 + j) * 16 + r;
+            if (row >= p.n) continue;
+            float y = 0.f, ss = 0.f;
+            if (cs == 1) {
+                y = sums[i];
+                if (p.eps > 0.f) ss = total_sq[t];
+            } else {
+                for (int c = 0; c < cs; ++c) {
+                    y += peer(sums + i, c);
+                    if (p.eps > 0.f) ss += peer(total_sq + t, c);
+                }
+            }
+            if (p.eps > 0.f) y *= 1.f / sqrtf(ss / float(p.k) + p.eps);
+            const long long at = t * p.ys + row;
+            if (p.add) y += value_of(p.add, at, p.yt);
+            if (p.yt == kF32) reinterpret_cast<float *>(p.y)[at] = y;
+            else if (p.yt == kF16) reinterpret_cast<__half *>(p.y)[at] = __float2half(y);
+            else reinterpret_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16(y);
+        }
+        if (cs > 1) cluster_sync();   // the others have read this CTA's sums
     }
 }
 
-static_assert((kXBytes / (3 * kInt4MaxTokens) - 64) / 2 >= 64 * kWarps, "a chunk of x is never empty");
-constexpr int smem_bytes(int nt) { return max(kXBytes, 8 * nt * 16 * kWarps * 4); }
+static_assert((kXBytes / (3 * kInt4MaxTokens) - 64) / 128 >= 8, "a chunk of x is never empty");
 
 template <bool BF, int PARTS, int NT>
 cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
 {
+    using C = MvCfg<NT>;
+    static_assert(C::kFixed + kXBytes + 4096 <= 227 * 1024, "");
     if (set)
-        return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(NT));
-    // columns of x that fit, a multiple of 64 for each warp
-    const int cols = p.tokens * PARTS;
-    int chunk = (kXBytes / cols - 64) / 2 / (64 * kWarps) * (64 * kWarps);
-    if (chunk > p.ku * 64) chunk = (p.ku * 64 + 511) / 512 * 512;
-    const int bytes = max(cols * (chunk + 32) * 2, 8 * NT * 16 * kWarps * 4);
-    k_matvec<BF, PARTS, NT><<<(p.n + 15) / 16, kThreadsMv, bytes, st>>>(p, chunk);
-    return cudaGetLastError();
+        return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kFixed + kXBytes);
+    const int cols = p.tokens * PARTS, tiles = (p.n + 15) / 16;
+    int cs = 1;
+    while (cs < kMaxCluster && cols * (p.ku / cs) * 128 > kShareX && p.ku / cs >= 2) cs *= 2;
+    int chunk = (kXBytes / cols - 64) / 128;   // units of 64 columns that fit
+    if (chunk > (p.ku + cs - 1) / cs) chunk = (p.ku + cs - 1) / cs;
+    int clusters = cs == 1 ? p.n_sm : p.clusters[cs == 2 ? 0 : cs == 4 ? 1 : 2];
+    if (clusters > tiles) clusters = tiles;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(clusters * cs);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kFixed + cols * (chunk * 64 + 32) * 2;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cs > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_matvec<BF, PARTS, NT>, p, cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3, clusters, chunk);
 }
 
 template <bool BF, int PARTS>
@@ -274,6 +429,26 @@ cudaError_t int4_setup()
             const cudaError_t e = dispatch(p, nullptr, true);
             if (e != cudaSuccess) return e;
         }
+    return cudaSuccess;
+}
+
+cudaError_t int4_clusters(int (&clusters)[3])
+{
+    for (int i = 0; i < 3; ++i) {
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2 << i);
+        cfg.blockDim = dim3(MvCfg<4>::kThreads);
+        cfg.dynamicSmemBytes = MvCfg<4>::kFixed + kXBytes;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], k_matvec<true, 3, 4>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (clusters[i] < 1) clusters[i] = 1;
+    }
     return cudaSuccess;
 }
 
