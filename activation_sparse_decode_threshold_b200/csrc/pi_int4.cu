@@ -13,9 +13,8 @@
 namespace pi {
 namespace {
 
-constexpr int kXBytes = 104 * 1024;    // shared memory for a chunk of x: 512 columns of 96 parts at least
 constexpr int kMaxCluster = 8;
-constexpr int kShareX = 64 * 1024;     // a CTA's part of x above this: the columns are split over more CTAs
+constexpr int kShareX = 112 * 1024;     // a CTA's part of x above this: the columns are split over more CTAs
 
 // Unit (row tile, 64 columns): lane (g = lane / 4, t = lane % 4) finds at 16 lane
 // the eight columns 8t .. 8t+7 of rows g and g + 8, first of the unit's first
@@ -46,72 +45,71 @@ __global__ void k_pack(const uint8_t *q, const uint16_t *s, uint8_t *dst, int n,
     reinterpret_cast<uint16_t *>(out + 512)[g * 4 + t] = row < n && c < k ? s[row * (k / 32) + c / 32] : uint16_t(0);
 }
 
-template <bool BF>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+// d = A B + d, or (ADD false) A B.
+template <bool BF, bool ADD>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
+    const float c0 = ADD ? d[0] : 0.f, c1 = ADD ? d[1] : 0.f, c2 = ADD ? d[2] : 0.f, c3 = ADD ? d[3] : 0.f;
     if (BF)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                     "{%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                     "{%8, %9}, {%10, %11, %12, %13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                     "{%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                     "{%8, %9}, {%10, %11, %12, %13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Eight nibbles to four 16-bit pairs n - 8: a nibble under the exponent bits of
-// 1024 (fp16) or 128 (bf16) is that number plus n.
+// (v & mask) | bits, in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
+    return r;
+}
+
+// Eight nibbles to four 16-bit pairs n - 8.  Under the exponent bits of 1024
+// (fp16) or 128 (bf16) a nibble is that number plus n; in fp16 one four bits
+// further up is 1024 + 16 n, which a product and a sum bring to n - 8 without a
+// shift.  All of it is exact.
 template <bool BF>
 __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&r)[4])
 {
-    constexpr uint32_t magic = BF ? 0x43004300u : 0x64006400u;
+    if (BF) {
+        const uint32_t bias = 0x43084308u;   // 136
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | magic;
-        if (BF) {
-            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __floats2bfloat162_rn(136.f, 136.f));
-            r[i] = *reinterpret_cast<const uint32_t *>(&d);
-        } else {
-            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), __floats2half2_rn(1032.f, 1032.f));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
+            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&bias));
             r[i] = *reinterpret_cast<const uint32_t *>(&d);
         }
-    }
-}
-
-__device__ __forceinline__ void load8(const uint8_t *x, long long i, int xt, float (&v)[8])
-{
-    if (xt == kF32) {
-        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(x + 2 * i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t bias = 0x64086408u, part = 0x2c002c00u, bias2 = 0xd480d480u;   // 1032; 1/16, -72
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = xt == kF16 ? __half22float2(*reinterpret_cast<const __half2 *>(&u[e]))
-                                        : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e]));
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t z = w >> (8 * i), v = and_or(z, 0x000f000fu, 0x64006400u), u = and_or(z, 0x00f000f0u, 0x64006400u);
+            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&bias));
+            const __half2 e = __hfma2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&part),
+                                      *reinterpret_cast<const __half2 *>(&bias2));
+            r[2 * i] = *reinterpret_cast<const uint32_t *>(&d);
+            r[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&e);
         }
     }
 }
 
-// The matrix is read once: past L1, and first to leave L2.
-__device__ __forceinline__ uint4 ldg_stream(const uint4 *p)
+__device__ __forceinline__ void load8(const uint8_t *x, long long i, float (&v)[8])
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+    const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(x) + i);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ uint2 ldg_stream(const uint2 *p)
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src)
 {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -145,10 +143,12 @@ template <int NT>
 struct MvCfg {
     static constexpr int kWarps = NT <= 4 ? 16 : 8;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kAhead = 4;                                // units in flight for each warp
+    static constexpr int kBatch = 4;                                // units that a warp takes from its ring at once
     static constexpr int kSlot = 16 * 8 * NT;                       // sums of a warp for one row tile
-    static constexpr int kSums = kWarps * 16 * kInt4MaxTokens;      // of a CTA's row tiles: [tile][token][row]
-    static constexpr int kFixed = (2 * kWarps * kSlot + kSums) * 4; // bytes before the chunk of x
+    // Bytes: slots; rings of `depth` batches; sums of a CTA's row tiles, [tile][token][row]; behind them the chunk of x.
+    static constexpr int kSlots = 2 * kWarps * kSlot * 4, kRing = kBatch * kInt4Unit, kSum = kWarps * 16 * 4;
+    static constexpr int fixed(int depth, int tokens) { return kSlots + kWarps * kRing * depth + kSum * tokens; }
+    static constexpr int kRoom = 222 * 1024;
 };
 
 // A cluster takes row tiles (of 16), up to kWarps at a time; its CTAs share the
@@ -156,22 +156,24 @@ struct MvCfg {
 // shared out evenly over its warps, so that a warp has parts of two tiles at
 // most: the sums of these go to two slots in shared memory, from there in order
 // to the tile's sums, and from the CTAs, in order, to y.  Bound by the matrix's
-// bytes: each warp keeps kAhead units of 576 bytes under way in registers, and x
+// bytes: each warp keeps two or three batches of 4 units of 576 bytes under way, and x
 // is brought to each CTA once (for 13 tokens of 8192 columns it is 213 KB, more
 // than the CTA's share of the matrix: hence the clusters).
 // PARTS: 3 for F32 x, else 1.  NT: tiles of 8 columns of B (tokens * PARTS).
 template <bool BF, int PARTS, int NT>
-__global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p, int log_cs, int clusters, int chunk)
+__global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p, int log_cs, int clusters, int chunk, int depth, int split)
 {
     using C = MvCfg<NT>;
-    constexpr int W = C::kWarps, T = C::kThreads, U = C::kAhead;
+    constexpr int W = C::kWarps, T = C::kThreads, U = C::kBatch;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float ssq[kInt4MaxTokens * W];
     __shared__ float total_sq[kInt4MaxTokens];
     __shared__ int from_warp[W], to_warp[W];   // of a tile: the slot of its first warp, its last warp
-    float *slots = reinterpret_cast<float *>(smem), *sums = slots + 2 * W * C::kSlot;
-    uint16_t *xs = reinterpret_cast<uint16_t *>(smem + C::kFixed);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
+    float *slots = reinterpret_cast<float *>(smem);
+    const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem + C::kSlots)) + warp * depth * C::kRing;
+    float *sums = reinterpret_cast<float *>(smem + C::kSlots + W * C::kRing * depth);
+    uint16_t *xs = reinterpret_cast<uint16_t *>(smem + C::fixed(depth, p.tokens));
     const int cols = p.tokens * PARTS, stride = chunk * 64 + 32;   // 64 bytes past a multiple of 128: no bank conflicts
     const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1), cluster = blockIdx.x >> log_cs;
     const int tiles = (p.n + 15) / 16;
@@ -188,25 +190,29 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
             const int first = min(warp, busy) * share + min(warp, rest), end = first + (warp < busy ? share + (warp < rest) : 0);
             // the first units are under way before x is
             const int tile = first / ks;
-            int k = first - tile * ks;
+            const int k = first - tile * ks;
+            // units not yet under way: `left` of this tile at `next`, then `later` of the one behind it
             const uint8_t *next = p.w + ((long long)(t0 + tile) * p.ku + k0 + k) * kInt4Unit;
-            const long long jump = (long long)(p.ku - ks) * kInt4Unit;
-            int next_k = k, ahead = first;
-            uint4 wq[U];
-            uint2 ws[U];
-            auto load = [&](int i) {
-                if (ahead >= end) return;
-                wq[i] = ldg_stream(reinterpret_cast<const uint4 *>(next + 16 * lane));
-                ws[i] = ldg_stream(reinterpret_cast<const uint2 *>(next + 512 + 8 * g));
-                ++ahead;
-                next += kInt4Unit;
-                if (++next_k == ks) {
-                    next_k = 0;
-                    next += jump;
+            const uint8_t *behind = p.w + ((long long)(t0 + tile + 1) * p.ku + k0) * kInt4Unit;
+            int left = min(end - first, ks - k), later = end - first - left, put = 0, get = 0;
+            const int first_len = left, second_len = later;
+            auto issue = [&]() {   // the next batch: U units, or the rest of a tile
+                const int pieces = min(U, left) * (kInt4Unit / 16);
+                const uint32_t dst = ring + put * (U * kInt4Unit);
+#pragma unroll
+                for (int i = 0; i < (U * kInt4Unit / 16 + 31) / 32; ++i)
+                    if (lane + 32 * i < pieces) copy_async(dst + 16 * (lane + 32 * i), next + 16 * (lane + 32 * i));
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                put = put + 1 == depth ? 0 : put + 1;
+                next += U * kInt4Unit;
+                left -= min(U, left);
+                if (left == 0) {
+                    next = behind;
+                    left = later;
+                    later = 0;
                 }
             };
-#pragma unroll
-            for (int i = 0; i < U; ++i) load(i);
+            for (int i = 1; i < depth; ++i) issue();
             // a tile belongs to the warps from the one with its first unit on
             if (lane == 0 && first < end) {
                 const int last = (end - 1 - first + k) / ks;   // 1: the warp goes on into a second tile
@@ -216,47 +222,52 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                 if (last && first + 2 * ks - k <= end) to_warp[tile + 1] = warp;
             }
             if (t0 == t_begin || !one_pass) {
+                // a warp for each token, or for each of `split` parts of it; the squares on the way
                 const int pieces = ks * 8;   // of 8 columns
-#pragma unroll 2
-                for (int i = threadIdx.x; i < p.tokens * pieces; i += T) {
-                    const int t = i / pieces, at = (i - t * pieces) * 8, col = k0 * 64 + at;
-                    uint16_t *dst = xs + t * stride + at;
-                    if (PARTS == 1) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (col < p.k) w = *reinterpret_cast<const uint4 *>(p.x + 2 * (t * p.xs + col));
-                        *reinterpret_cast<uint4 *>(dst) = w;
-                    } else {
-                        float v[8] = {};
-                        if (col < p.k) load8(p.x, t * p.xs + col, p.xt, v);
+                for (int i = warp; i < p.tokens * split; i += W) {
+                    const int t = i / split, part_of = i - t * split;
+                    uint16_t *row = xs + t * stride;
+                    float ss = 0.f;
+                    const bool squares = p.eps > 0.f && t0 == t_begin;
+#pragma unroll 4
+                    for (int c = part_of * 32 + lane; c < pieces; c += 32 * split) {
+                        const int col = k0 * 64 + 8 * c;
+                        if (PARTS == 1) {
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            if (col < p.k) w = *reinterpret_cast<const uint4 *>(p.x + 2 * (t * p.xs + col));
+                            *reinterpret_cast<uint4 *>(row + 8 * c) = w;
+                            if (squares) {
+                                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int part = 0; part < PARTS; ++part) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float c = cut(v[e]);
-                                const uint32_t b = isnan(v[e]) ? 0x7fc0u : __float_as_uint(v[e]) >> 16;
-                                u[e / 2] = e & 1 ? u[e / 2] | (b << 16) : b;
-                                v[e] = isfinite(v[e]) ? v[e] - c : 0.f;
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = BF ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e]))
+                                                        : __half22float2(*reinterpret_cast<const __half2 *>(&u[e]));
+                                    ss += f.x * f.x;
+                                    ss += f.y * f.y;
+                                }
                             }
-                            *reinterpret_cast<uint4 *>(dst + part * p.tokens * stride) = make_uint4(u[0], u[1], u[2], u[3]);
+                        } else {
+                            float v[8] = {};
+                            if (col < p.k) load8(p.x, t * p.xs + col, v);
+                            if (squares) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+                            }
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part) {
+                                uint32_t u[4];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float cutoff = cut(v[e]);
+                                    const uint32_t b = isnan(v[e]) ? 0x7fc0u : __float_as_uint(v[e]) >> 16;
+                                    u[e / 2] = e & 1 ? u[e / 2] | (b << 16) : b;
+                                    v[e] = isfinite(v[e]) ? v[e] - cutoff : 0.f;
+                                }
+                                *reinterpret_cast<uint4 *>(row + part * p.tokens * stride + 8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
                         }
                     }
-                }
-                if (p.eps > 0.f && t0 == t_begin) {
-                    // sums of squares: one warp for each token, or for each of several pieces of it
-                    const int split = max(1, W / p.tokens);
-                    for (int i = warp; i < p.tokens * split; i += W) {
-                        const int t = i / split, piece = i - t * split;
-                        float ss = 0.f;
-#pragma unroll 2
-                        for (int c = piece * 32 + lane; c < pieces; c += 32 * split) {
-                            const int col = k0 * 64 + 8 * c;
-                            if (col >= p.k) break;
-                            float v[8];
-                            load8(p.x, t * p.xs + col, p.xt, v);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-                        }
+                    if (squares) {
 #pragma unroll
                         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
                         if (lane == 0) ssq[i] = ss;
@@ -264,7 +275,6 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                 }
                 __syncthreads();
                 if (p.eps > 0.f && t0 == t_begin && threadIdx.x < p.tokens) {
-                    const int split = max(1, W / p.tokens);
                     float ss = k0 == k_begin ? 0.f : total_sq[threadIdx.x];
                     for (int i = 0; i < split; ++i) ss += ssq[threadIdx.x * split + i];
                     total_sq[threadIdx.x] = ss;
@@ -273,116 +283,142 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
 
             // ---- the warp's units
             float acc[NT][4] = {};
-            float *slot = slots + 2 * warp * C::kSlot;
-            auto flush = [&]() {
+            const uint16_t *xb[NT];
 #pragma unroll
-                for (int nt2 = 0; nt2 < NT; ++nt2) {
-                    *reinterpret_cast<float2 *>(slot + g * 8 * NT + nt2 * 8 + 2 * t4) = make_float2(acc[nt2][0], acc[nt2][1]);
-                    *reinterpret_cast<float2 *>(slot + (g + 8) * 8 * NT + nt2 * 8 + 2 * t4) = make_float2(acc[nt2][2], acc[nt2][3]);
-                    acc[nt2][0] = acc[nt2][1] = acc[nt2][2] = acc[nt2][3] = 0.f;
-                }
-                slot += C::kSlot;
-            };
-            for (int u = first; u < end;) {
+            for (int n8 = 0; n8 < NT; ++n8) xb[n8] = xs + min(n8 * 8 + g, cols - 1) * stride + k * 64 + t4 * 8;
+#pragma unroll 1
+            for (int seg = 0; seg < 2; ++seg) {
+                const int len = seg ? second_len : first_len;
+                if (len == 0) break;
+                for (int done = 0; done < len; done += U) {
+                    issue();
+                    if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+                    else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    __syncwarp();
+                    const uint32_t units = ring + get * (U * kInt4Unit);
+                    const int have = min(U, len - done);
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    if (u >= end) break;
-                    const uint32_t qq[4] = {wq[i].x, wq[i].y, wq[i].z, wq[i].w}, sp[2] = {ws[i].x, ws[i].y};
-                    load(i);
+                    for (int i = 0; i < U; ++i) {
+                        if (i >= have) break;
+                        uint32_t qq[4], sp[2];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(qq[0]), "=r"(qq[1]), "=r"(qq[2]), "=r"(qq[3]) : "r"(units + i * kInt4Unit + 16 * lane));
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(sp[0]), "=r"(sp[1]) : "r"(units + i * kInt4Unit + 512 + 8 * g));
 #pragma unroll
-                    for (int grp = 0; grp < 2; ++grp) {
-                        uint32_t lo[4], hi[4];
-                        nibbles<BF>(qq[2 * grp], lo);
-                        nibbles<BF>(qq[2 * grp + 1], hi);
-                        const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&sp[grp]));
+                        for (int grp = 0; grp < 2; ++grp) {
+                            uint32_t lo[4], hi[4];
+                            nibbles<BF>(qq[2 * grp], lo);
+                            nibbles<BF>(qq[2 * grp + 1], hi);
+                            const float2 sc = __half22float2(*reinterpret_cast<const __half2 *>(&sp[grp]));
 #pragma unroll
-                        for (int n8 = 0; n8 < NT; ++n8) {
-                            const int col = min(n8 * 8 + g, cols - 1);
-                            const uint4 b = *reinterpret_cast<const uint4 *>(xs + col * stride + k * 64 + grp * 32 + t4 * 8);
-                            float c[4] = {};
-                            mma16816<BF>(c, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                            mma16816<BF>(c, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-                            acc[n8][0] += sc.x * c[0];
-                            acc[n8][1] += sc.x * c[1];
-                            acc[n8][2] += sc.y * c[2];
-                            acc[n8][3] += sc.y * c[3];
+                            for (int n8 = 0; n8 < NT; ++n8) {
+                                const uint4 b = *reinterpret_cast<const uint4 *>(xb[n8] + i * 64 + grp * 32);
+                                float c[4];
+                                mma16816<BF, false>(c, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                                mma16816<BF, true>(c, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                                acc[n8][0] += sc.x * c[0];
+                                acc[n8][1] += sc.x * c[1];
+                                acc[n8][2] += sc.y * c[2];
+                                acc[n8][3] += sc.y * c[3];
+                            }
                         }
                     }
-                    ++u;
-                    if (++k == ks) {
-                        k = 0;
-                        flush();
-                    }
+                    __syncwarp();   // the batch has been read
+                    get = get + 1 == depth ? 0 : get + 1;
+#pragma unroll
+                    for (int n8 = 0; n8 < NT; ++n8) xb[n8] += have * 64;
+                }
+                float *slot = slots + (2 * warp + seg) * C::kSlot;
+#pragma unroll
+                for (int n8 = 0; n8 < NT; ++n8) {
+                    *reinterpret_cast<float2 *>(slot + g * 8 * NT + n8 * 8 + 2 * t4) = make_float2(acc[n8][0], acc[n8][1]);
+                    *reinterpret_cast<float2 *>(slot + (g + 8) * 8 * NT + n8 * 8 + 2 * t4) = make_float2(acc[n8][2], acc[n8][3]);
+                    acc[n8][0] = acc[n8][1] = acc[n8][2] = acc[n8][3] = 0.f;
+                    xb[n8] -= ks * 64;   // (the second tile starts at the first column)
                 }
             }
-            if (k != 0 && first < end) flush();
             __syncthreads();
             // ---- the tiles' sums: warps in order, parts from the least
-            for (int i = threadIdx.x; i < nt * 16 * p.tokens; i += T) {
-                const int r = i % 16, j = i / 16 % nt, t = i / 16 / nt;
-                float y = k0 == k_begin ? 0.f : sums[(j * p.tokens + t) * 16 + r];
-                const int s0 = from_warp[j], s1 = 2 * to_warp[j];
-                const float *src = slots + s0 * C::kSlot + r * 8 * NT + t;
-#pragma unroll
-                for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
-                src = slots + (s0 / 2 + 1) * 2 * C::kSlot + r * 8 * NT + t;
-#pragma unroll 4
-                for (int w = s0 / 2 + 1; w <= s1 / 2; ++w, src += 2 * C::kSlot) {
+            if (warp < nt) {   // a warp for each tile
+                const int from = from_warp[warp], more = to_warp[warp] - from / 2, r = lane % 16;
+                for (int t = lane / 16; t < p.tokens; t += 2) {
+                    float *sum = sums + (warp * p.tokens + t) * 16 + r;
+                    float y = k0 == k_begin ? 0.f : *sum;
+                    const float *src = slots + from * C::kSlot + r * 8 * NT + t;
 #pragma unroll
                     for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
+                    src = slots + (from / 2 + 1) * 2 * C::kSlot + r * 8 * NT + t;
+#pragma unroll 4
+                    for (int w = 0; w < more; ++w, src += 2 * C::kSlot) {
+#pragma unroll
+                        for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
+                    }
+                    *sum = y;
                 }
-                sums[(j * p.tokens + t) * 16 + r] = y;
             }
             if (cs == 1 || k0 + chunk < k_end) __syncthreads();
         }
         // ---- over the cluster's CTAs, in order, to y
+        // each CTA has its part of the tiles; a half warp for 16 rows of a token
+        const int j_begin = nt * rank >> log_cs, pairs = ((nt * (rank + 1) >> log_cs) - j_begin) * p.tokens;
+        auto place = [&](int i, int &sum, int &t) {   // y's element (or -1), the sum's place, the token
+            const int j = j_begin + i / p.tokens, row = (t0 + j) * 16 + lane % 16;
+            t = i % p.tokens;
+            sum = (j * p.tokens + t) * 16 + lane % 16;
+            return i < pairs && row < p.n ? t * p.ys + row : -1;
+        };
+        int i = 2 * warp + lane / 16, sum, t;
+        long long at = place(i, sum, t);
+        float add = p.add && at >= 0 ? value_of(p.add, at, p.yt) : 0.f;   // under way while the CTAs wait for each other
         if (cs > 1) cluster_sync();
-        const int all = nt * 16 * p.tokens;
-        for (int i = (all * rank >> log_cs) + threadIdx.x; i < all * (rank + 1) >> log_cs; i += T) {
-            const int r = i % 16, t = i / 16 % p.tokens, j = i / 16 / p.tokens;
-            const long long row = (long long)(t0 + j) * 16 + r;
-            if (row >= p.n) continue;
+        for (; i < pairs; i += 2 * W) {
             float y = 0.f, ss = 0.f;
             if (cs == 1) {
-                y = sums[i];
+                y = sums[sum];
                 if (p.eps > 0.f) ss = total_sq[t];
             } else {
                 for (int c = 0; c < cs; ++c) {
-                    y += peer(sums + i, c);
+                    y += peer(sums + sum, c);
                     if (p.eps > 0.f) ss += peer(total_sq + t, c);
                 }
             }
             if (p.eps > 0.f) y *= 1.f / sqrtf(ss / float(p.k) + p.eps);
-            const long long at = t * p.ys + row;
-            if (p.add) y += value_of(p.add, at, p.yt);
-            if (p.yt == kF32) reinterpret_cast<float *>(p.y)[at] = y;
-            else if (p.yt == kF16) reinterpret_cast<__half *>(p.y)[at] = __float2half(y);
-            else reinterpret_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16(y);
+            if (p.add) y += add;
+            if (at >= 0) {
+                if (p.yt == kF32) reinterpret_cast<float *>(p.y)[at] = y;
+                else if (p.yt == kF16) reinterpret_cast<__half *>(p.y)[at] = __float2half(y);
+                else reinterpret_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16(y);
+            }
+            at = place(i + 2 * W, sum, t);
+            if (p.add && at >= 0) add = value_of(p.add, at, p.yt);
         }
         if (cs > 1) cluster_sync();   // the others have read this CTA's sums
     }
 }
 
-static_assert((kXBytes / (3 * kInt4MaxTokens) - 64) / 128 >= 8, "a chunk of x is never empty");
-
 template <bool BF, int PARTS, int NT>
 cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
 {
     using C = MvCfg<NT>;
-    static_assert(C::kFixed + kXBytes + 4096 <= 227 * 1024, "");
-    if (set)
-        return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kFixed + kXBytes);
+    static_assert((C::kRoom - C::fixed(2, kInt4MaxTokens)) / (8 * NT) >= 64 + 4 * 128, "a chunk of x has 4 units at least");
+    if (set) return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRoom);
     const int cols = p.tokens * PARTS, tiles = (p.n + 15) / 16;
     int cs = 1;
     while (cs < kMaxCluster && cols * (p.ku / cs) * 128 > kShareX && p.ku / cs >= 2) cs *= 2;
-    int chunk = (kXBytes / cols - 64) / 128;   // units of 64 columns that fit
-    if (chunk > (p.ku + cs - 1) / cs) chunk = (p.ku + cs - 1) / cs;
+    // the deepest rings that leave room for x's columns at once, or else for a part of them
+    const int units = (p.ku + cs - 1) / cs;
+    int depth = 4;
+    while (depth > 2 && C::fixed(depth, p.tokens) + cols * (units * 128 + 64) > C::kRoom) --depth;
+    int chunk = ((C::kRoom - C::fixed(depth, p.tokens)) / cols - 64) / 128;
+    if (chunk > units) chunk = units;
     int clusters = cs == 1 ? p.n_sm : p.clusters[cs == 2 ? 0 : cs == 4 ? 1 : 2];
     if (clusters > tiles) clusters = tiles;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(clusters * cs);
     cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kFixed + cols * (chunk * 64 + 32) * 2;
+    cfg.dynamicSmemBytes = C::fixed(depth, p.tokens) + cols * (chunk * 64 + 32) * 2;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -390,7 +426,8 @@ cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_matvec<BF, PARTS, NT>, p, cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3, clusters, chunk);
+    return cudaLaunchKernelEx(&cfg, k_matvec<BF, PARTS, NT>, p, cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3, clusters, chunk, depth,
+                              p.tokens < C::kWarps ? C::kWarps / p.tokens : 1);
 }
 
 template <bool BF, int PARTS>
@@ -442,7 +479,7 @@ cudaError_t int4_clusters(int (&clusters)[3])
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2 << i);
         cfg.blockDim = dim3(MvCfg<4>::kThreads);
-        cfg.dynamicSmemBytes = MvCfg<4>::kFixed + kXBytes;
+        cfg.dynamicSmemBytes = MvCfg<4>::kRoom;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], k_matvec<true, 3, 4>, &cfg);

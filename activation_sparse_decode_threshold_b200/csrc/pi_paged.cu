@@ -108,19 +108,29 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     return r;
 }
 
+// d = A B + c
 template <bool BF>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint2 b)
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2 b, float c0, float c1, float c2, float c3)
 {
     if (BF)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                     "{%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+                     "{%8, %9}, {%10, %11, %12, %13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                     "{%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+                     "{%8, %9}, {%10, %11, %12, %13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2 b) { mma<BF>(d, a, b, d[0], d[1], d[2], d[3]); }
+// The first product of a sum.
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2 b, bool first)
+{
+    if (first) mma<BF>(d, a, b, 0.f, 0.f, 0.f, 0.f);
+    else mma<BF>(d, a, b);
 }
 
 // A number as its 16-bit rounding (low half) and the rounding of what is left (high half).
@@ -151,6 +161,14 @@ __device__ __forceinline__ uint32_t hfma(uint32_t v, uint32_t a, uint32_t b)
                               *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
+// (v & mask) | bits, in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
+    return r;
+}
+
 // Two bytes of w (signed, with the top bit flipped) as an fp16 pair: under the
 // exponent of 1024 a byte b is 1024 + b.
 template <uint32_t SEL>
@@ -605,8 +623,9 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         const float f0 = half_of(ks[2 * rt], j), f1 = half_of(ks[2 * rt + 1], j);
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            float c[4] = {bias[FMT == kI4 ? j : 0][b], 0.f, bias[FMT == kI4 ? j : 0][b], 0.f};
-                            mma<false>(c, a0, query(2 * j, b));
+                            const float off = bias[FMT == kI4 ? j : 0][b];
+                            float c[4];
+                            mma<false>(c, a0, query(2 * j, b), off, 0.f, off, 0.f);
                             mma<false>(c, a1, query(2 * j + 1, b));
                             x[b][2 * rt] += f0 * (c[0] + c[1]);
                             x[b][2 * rt + 1] += f1 * (c[2] + c[3]);
@@ -615,7 +634,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                 }
         } else {
             constexpr int CC = NB * R == 1 ? 2 : 1;   // independent sums, where there are few products to fill the pipe with
-            float c[NB][R][CC][4] = {};
+            float c[NB][R][CC][4];
 #pragma unroll
             for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -630,14 +649,14 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         const uint32_t a1[4] = {bytes<0x4140>(r[2]), bytes<0x4140>(r[3]), bytes<0x4342>(r[2]), bytes<0x4342>(r[3])};
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            mma<false>(c[b][rt][0], a0, query(i, b));
-                            mma<false>(c[b][rt][CC - 1], a1, query(i + 1 < KS ? i + 1 : i, b));
+                            mma<false>(c[b][rt][0], a0, query(i, b), i == 0);
+                            mma<false>(c[b][rt][CC - 1], a1, query(i + 1 < KS ? i + 1 : i, b), i == 0 && CC == 2);
                         }
                     } else {
                         uint32_t r[4];
                         ldm4<false>(base + 16 * place(mat_row + 16 * rt, 2 * i + mat_piece), r);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) mma<BF>(c[b][rt][i % CC], r, query(i, b));
+                        for (int b = 0; b < NB; ++b) mma<BF>(c[b][rt][i % CC], r, query(i, b), i < CC);
                     }
                 }
 #pragma unroll
@@ -749,10 +768,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 #pragma unroll
                         for (int o = 0; o < 2; ++o) {
                             const uint32_t w = r[2 * h + o], z = w >> 8;
-                            a[0][2 * o] = hsub((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                            a[0][2 * o + 1] = hfma((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
-                            a[1][2 * o] = hsub((z & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                            a[1][2 * o + 1] = hfma((z & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+                            a[0][2 * o] = hsub(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);
+                            a[0][2 * o + 1] = hfma(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+                            a[1][2 * o] = hsub(and_or(z, 0x000f000fu, 0x64006400u), 0x64086408u);
+                            a[1][2 * o + 1] = hfma(and_or(z, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
                         }
                         const float f0 = f * half_of(vs[2 * rt], j), f1 = f * half_of(vs[2 * rt + 1], j);
 #pragma unroll
