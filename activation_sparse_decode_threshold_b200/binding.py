@@ -273,43 +273,49 @@ def pi_predict_noalloc(d_model, d_ff, rank, pred_dtype, threshold, V, U, bias, x
 # ---------------------------------------------------------------------------
 KV_LAYOUT = {"hnd": 0, "nhd": 1}
 _desc: dict = {}     # handle -> what the checks need of it
-_types: dict = {}    # torch's types, once a tensor has been seen
-_raw_stream = None
+_native_module = None
+EXT_PATH = os.path.join(HERE, "_pi_torch.so")
 
 
-def _torch_types():
-    """torch is imported by the first call that is given a tensor, as everywhere in this file."""
-    global _raw_stream
-    if not _types:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-            (lambda device: torch.cuda.current_stream(device).cuda_stream)
-        _types.update(float={torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}, f32=torch.float32, f16=torch.float16,
-                      bf16=torch.bfloat16, i8=torch.int8, u8=torch.uint8, i32=torch.int32)
-    return _types
+def _native():
+    """The native part (csrc/pi_torch.cpp), bound to the loaded library; raises if it was never built."""
+    global _native_module
+    if _native_module is None:
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError(f"{EXT_PATH} is missing: build it with "
+                               "`python -m activation_sparse_decode_threshold_b200.build`")
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries come first)
+        loader = importlib.machinery.ExtensionFileLoader("_pi_torch", EXT_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pi_torch", loader))
+        loader.exec_module(module)
+        module.init(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value
+                      for f in ("pi_int4_matvec", "pi_kv_append", "pi_kv_read", "pi_paged_attention")))
+        _native_module = module
+    return _native_module
 
 
 def _bad(where: str, msg: str):
     raise PiError(PI_ERR_INVALID_ARG, where, msg)
 
 
-def _float_code(t, where: str, name: str) -> int:
-    code = _torch_types()["float"].get(t.dtype)
-    if code is None:
-        _bad(where, f"{name} must be float32, float16 or bfloat16")
-    return code
+def _fail(result, where: str):
+    """What a native call returned instead of None: a status, or the text of a refusal."""
+    if isinstance(result, str):
+        _bad(where, result)
+    _check(result, where)
 
 
-def _off_device(where: str, name: str, device: int):
-    _bad(where, f"{name} is not on cuda:{device}")
+def _stream_arg(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _stream_on(stream, device: int):
     if stream is None:
-        if _raw_stream is None:
-            _torch_types()
-        return _raw_stream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
 
 
 def _handle_desc(h, kind: str, where: str):
@@ -321,20 +327,21 @@ def _handle_desc(h, kind: str, where: str):
 
 def pi_int4_create(q, s, device=None, stream=None) -> int:
     """`q`: uint8 [n_rows x n_cols/2] nibbles, `s`: float16 [n_rows x n_cols/32], both contiguous on the device."""
-    w, ty = "pi_int4_create", _torch_types()
+    import torch
+    w = "pi_int4_create"
     if not (q.is_cuda and s.is_cuda):
         _bad(w, "q and s must be CUDA tensors")
     device = q.get_device() if device is None else device
     if q.get_device() != device or s.get_device() != device:
-        _off_device(w, "q or s", device)
-    if q.dim() != 2 or q.dtype != ty["u8"] or not q.is_contiguous():
+        _bad(w, f"q or s is not on cuda:{device}")
+    if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_contiguous():
         _bad(w, "q must be contiguous uint8 [n, k/2]")
     n, k = q.shape[0], 2 * q.shape[1]
-    if k % 32 or s.dtype != ty["f16"] or not s.is_contiguous() or s.shape != (n, k // 32):
+    if k % 32 or s.dtype != torch.float16 or not s.is_contiguous() or s.shape != (n, k // 32):
         _bad(w, "s must be contiguous float16 [n, k/32]")
-    h = ctypes.c_void_p()
+    call, h = _native().matvec, ctypes.c_void_p()
     _check(lib().pi_int4_create(n, k, q.data_ptr(), s.data_ptr(), device, _stream_on(stream, device), ctypes.byref(h)), w)
-    _desc[h.value] = {"kind": "int4", "n": n, "k": k, "device": device}
+    _desc[h.value] = {"kind": "int4", "shape": (n, k, device), "call": call}
     return h.value
 
 
@@ -343,34 +350,13 @@ def pi_int4_destroy(m: int):
         lib().pi_int4_destroy(m)
 
 
-def _token_rows(t, where: str, name: str, device: int, shape: tuple, inner: tuple) -> int:
-    """Row distance of a tensor on `device` of this shape, [tokens, ...], whose rows are contiguous (strides `inner`)."""
-    st = t.stride()
-    if t.shape != shape:
-        _bad(where, f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if st[1:] != inner and any(n != 1 and a != b for n, a, b in zip(shape[1:], st[1:], inner)):
-        _bad(where, f"{name}: a token's values must be contiguous")
-    if t.get_device() != device:
-        _off_device(where, name, device)
-    return st[0]
-
-
 def pi_int4_matvec(m, x, y, add=None, norm_eps=0.0, stream=None):
     """y [tokens x n_rows] = add + W f(x), x [tokens x n_cols]."""
-    w = "pi_int4_matvec"
-    d = _handle_desc(m, "int4", w)
-    device, tokens = d["device"], x.shape[0]
-    xs = _token_rows(x, w, "x", device, (tokens, d["k"]), (1,))
-    ys = _token_rows(y, w, "y", device, (tokens, d["n"]), (1,))
-    xc, yc, ap = _float_code(x, w, "x"), _float_code(y, w, "y"), None
-    if add is not None:
-        if add is not y and ((_token_rows(add, w, "add", device, (tokens, d["n"]), (1,)) != ys and tokens != 1)
-                             or add.dtype != y.dtype):
-            _bad(w, "add must have y's type and row distance")
-        ap = add.data_ptr()
-    st = lib().pi_int4_matvec(m, tokens, xc, x.data_ptr(), xs, ap, yc, y.data_ptr(), ys, norm_eps, _stream_on(stream, device))
-    if st:
-        _check(st, w)
+    d = _handle_desc(m, "int4", "pi_int4_matvec")
+    n, k, device = d["shape"]
+    got = d["call"](m, n, k, device, x, y, add, norm_eps, stream if stream is None else _stream_arg(stream))
+    if got is not None:
+        _fail(got, "pi_int4_matvec")
 
 
 def pi_attn_create(n_heads, n_kv_heads, head_dim, cache_dtype="bf16", page_size=64, layout="hnd", rotary_dim=0,
@@ -384,10 +370,12 @@ def pi_attn_create(n_heads, n_kv_heads, head_dim, cache_dtype="bf16", page_size=
         _bad(w, f"unknown layout {layout!r}")
     desc = pi_attn_desc(n_heads, n_kv_heads, head_dim, code, page_size, KV_LAYOUT[layout], rotary_dim, int(rotary_pairs),
                         rope_theta, norm_eps, scale, softcap, window, device)
+    _native()
     h = ctypes.c_void_p()
     _check(lib().pi_attn_create(ctypes.byref(desc), ctypes.byref(h)), w)
     _desc[h.value] = {"kind": "attention", "heads": n_heads, "kv_heads": n_kv_heads, "dim": head_dim, "code": code,
-                      "page": page_size, "layout": layout, "device": device, "inner": (head_dim, 1)}
+                      "page": page_size, "layout": layout, "device": device,
+                      "layer": (h.value, n_heads, n_kv_heads, head_dim, device)}
     return h.value
 
 
@@ -409,16 +397,16 @@ class pi_kv_cache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.c = _kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
-        self.ref = ctypes.byref(self.c)
+        self.address = ctypes.addressof(self.c)
         self.checked = None
 
 
 def _cache_arg(cache, d, where):
     if cache.checked is not d:
-        ty = _torch_types()
-        row, dt, scale = {1: (d["dim"], ty["f16"], None), 2: (d["dim"], ty["bf16"], None),
-                          4: (d["dim"], ty["i8"], ((), ty["f32"])),
-                          3: (d["dim"] // 2, ty["u8"], ((d["dim"] // 32,), ty["f16"]))}[d["code"]]
+        import torch
+        row, dt, scale = {1: (d["dim"], torch.float16, None), 2: (d["dim"], torch.bfloat16, None),
+                          4: (d["dim"], torch.int8, ((), torch.float32)),
+                          3: (d["dim"] // 2, torch.uint8, ((d["dim"] // 32,), torch.float16))}[d["code"]]
         lead = (cache.k.shape[0], d["kv_heads"], d["page"]) if d["layout"] == "hnd" else \
             (cache.k.shape[0], d["page"], d["kv_heads"])
         for name in ("k", "v"):
@@ -431,99 +419,33 @@ def _cache_arg(cache, d, where):
             elif s is None or s.shape != (*lead, *scale[0]) or s.dtype != scale[1] or not s.is_contiguous():
                 _bad(where, f"cache {name}_scale must be contiguous {scale[1]} {[*lead, *scale[0]]}")
             if t.get_device() != d["device"] or (s is not None and s.get_device() != d["device"]):
-                _off_device(where, f"cache {name}", d["device"])
+                _bad(where, f"cache {name} is not on cuda:{d['device']}")
         cache.checked = d
-    return cache.ref
-
-
-def _table_arg(table, d, where):
-    sh, st = table.shape, table.stride()
-    if table.dtype != _types["i32"]:
-        _bad(where, "table must be int32")
-    if len(sh) != 2 or (st[1] != 1 and sh[1] != 1):
-        _bad(where, "table must be [sequences, pages] with contiguous rows")
-    if table.get_device() != d["device"]:
-        _off_device(where, "table", d["device"])
-    return ctypes.byref(_kv_table(table.data_ptr(), sh[0], sh[1], st[0]))
-
-
-def _ints(t, where, d, name, shape):
-    """Address of an int32 vector of this shape."""
-    if t.dtype != _torch_types()["i32"]:
-        _bad(where, f"{name} must be int32")
-    if t.shape != shape or len(shape) != 1 or (t.stride(0) != 1 and shape[0] != 1):
-        _bad(where, f"{name} must be contiguous {list(shape)}")
-    if t.get_device() != d["device"]:
-        _off_device(where, name, d["device"])
-    return t.data_ptr()
-
-
-def _norm_weight(t, where, d, name):
-    if t.dtype != _types["f32"] or not t.is_contiguous() or t.numel() != d["dim"]:
-        _bad(where, f"{name} must be contiguous float32 [head_dim]")
-    if t.get_device() != d["device"]:
-        _off_device(where, name, d["device"])
-    return t.data_ptr()
+    return cache.address
 
 
 def pi_kv_append(a, cache, table, pos, q, k, v, q_out, seq=None, q_norm=None, k_norm=None, stream=None):
     """q, q_out [tokens, heads, dim], k and v [tokens, kv heads, dim]; `pos` (and `seq`) int32 [tokens]."""
-    w = "pi_kv_append"
-    d = _handle_desc(a, "attention", w)
-    device, dim, inner = d["device"], d["dim"], d["inner"]
-    pp = _ints(pos, w, d, "pos", pos.shape)
-    sp = None if seq is None else _ints(seq, w, d, "seq", pos.shape)
-    tokens = pos.shape[0]
-    qsh, ksh, code = (tokens, d["heads"], dim), (tokens, d["kv_heads"], dim), _float_code(q, w, "q")
-    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
-        _bad(w, "q, k, v and q_out must have one type")
-    st = lib().pi_kv_append(
-        a, _cache_arg(cache, d, w), _table_arg(table, d, w), tokens, sp, pp, code,
-        q.data_ptr(), _token_rows(q, w, "q", device, qsh, inner), k.data_ptr(), _token_rows(k, w, "k", device, ksh, inner),
-        v.data_ptr(), _token_rows(v, w, "v", device, ksh, inner),
-        None if q_norm is None else _norm_weight(q_norm, w, d, "q_norm"),
-        None if k_norm is None else _norm_weight(k_norm, w, d, "k_norm"),
-        q_out.data_ptr(), _token_rows(q_out, w, "q_out", device, qsh, inner), _stream_on(stream, device))
-    if st:
-        _check(st, w)
+    d = _handle_desc(a, "attention", "pi_kv_append")
+    got = _native_module.append(d["layer"], _cache_arg(cache, d, "pi_kv_append"), table, pos, q, k, v, q_out, seq, q_norm, k_norm,
+                                stream if stream is None else _stream_arg(stream))
+    if got is not None:
+        _fail(got, "pi_kv_append")
 
 
 def pi_kv_read(a, cache, table, pos, k_out, v_out, seq=None, stream=None):
     """k_out and v_out: contiguous [tokens, kv heads, dim] of one type."""
-    w = "pi_kv_read"
-    d = _handle_desc(a, "attention", w)
-    device = d["device"]
-    pp = _ints(pos, w, d, "pos", pos.shape)
-    sp = None if seq is None else _ints(seq, w, d, "seq", pos.shape)
-    shape = (pos.shape[0], d["kv_heads"], d["dim"])
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t.shape != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
-            _bad(w, f"{name} must be contiguous {list(shape)}, both of one type")
-        if t.get_device() != device:
-            _off_device(w, name, device)
-    st = lib().pi_kv_read(a, _cache_arg(cache, d, w), _table_arg(table, d, w), shape[0], sp, pp, _float_code(k_out, w, "k_out"),
-                          k_out.data_ptr(), v_out.data_ptr(), _stream_on(stream, device))
-    if st:
-        _check(st, w)
+    d = _handle_desc(a, "attention", "pi_kv_read")
+    got = _native_module.read(d["layer"], _cache_arg(cache, d, "pi_kv_read"), table, pos, k_out, v_out, seq,
+                              stream if stream is None else _stream_arg(stream))
+    if got is not None:
+        _fail(got, "pi_kv_read")
 
 
 def pi_paged_attention(a, cache, table, lens, q, out, lse=None, stream=None):
     """q and out [sequences, heads, dim]; `lens` int32 [sequences]; `lse` float32 [sequences, heads] or None."""
-    w = "pi_paged_attention"
-    d = _handle_desc(a, "attention", w)
-    device, inner, n = d["device"], d["inner"], table.shape[0]
-    lp, code, shape = _ints(lens, w, d, "lens", (n,)), _float_code(q, w, "q"), (n, d["heads"], d["dim"])
-    if q.dtype != out.dtype:
-        _bad(w, "q and out must have one type")
-    qs, os_ = _token_rows(q, w, "q", device, shape, inner), _token_rows(out, w, "out", device, shape, inner)
-    ep = None
-    if lse is not None:
-        if lse.shape != shape[:2] or lse.dtype != _types["f32"] or not lse.is_contiguous():
-            _bad(w, "lse must be contiguous float32 [sequences, heads]")
-        if lse.get_device() != device:
-            _off_device(w, "lse", device)
-        ep = lse.data_ptr()
-    st = lib().pi_paged_attention(a, _cache_arg(cache, d, w), _table_arg(table, d, w), lp, code, q.data_ptr(), qs,
-                                  out.data_ptr(), os_, ep, _stream_on(stream, device))
-    if st:
-        _check(st, w)
+    d = _handle_desc(a, "attention", "pi_paged_attention")
+    got = _native_module.attend(d["layer"], _cache_arg(cache, d, "pi_paged_attention"), table, lens, q, out, lse,
+                                stream if stream is None else _stream_arg(stream))
+    if got is not None:
+        _fail(got, "pi_paged_attention")

@@ -1,4 +1,5 @@
-"""Build libpi_ffn.so (sm_100a) in-tree with nvcc.
+"""Build libpi_ffn.so (sm_100a) in-tree with nvcc, and _pi_torch.so, the
+binding's native part, with g++ against torch's headers.
 
 Usage: python -m activation_sparse_decode_threshold_b200.build [--force] [--verbose]
 """
@@ -14,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libpi_ffn.so")
+EXT = os.path.join(HERE, "_pi_torch.so")
 OBJ = os.path.join(ROOT, "_build")
 SOURCES = ["pi_decode_f16.cu", "pi_decode_bf16.cu", "pi_decode_i4f16.cu", "pi_decode_i4bf16.cu",
            "pi_decode_f16i8.cu", "pi_decode_bf16i8.cu", "pi_decode_i4i8.cu",
@@ -39,6 +41,20 @@ def _deps_newer(target: str, sources: list[str]) -> bool:
         if os.path.getmtime(s) > t:
             return True
     return False
+
+
+def _ext_cmd(src: str) -> list[str]:
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    if not os.path.isdir(cuda):
+        cuda = "/usr/local/cuda/include"
+    inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), cuda]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[a for d in inc for a in ("-isystem", d)], src, "-o", EXT + ".tmp", "-L" + os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -67,8 +83,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
 
+    ext_src = os.path.join(CSRC, "pi_torch.cpp")
+    ext_new = force or _deps_newer(EXT, [ext_src, os.path.join(ROOT, "include", "pi_ffn.h")])
+    if ext_new:
+        jobs.append(_ext_cmd(ext_src))
+
     with ThreadPoolExecutor(max_workers=min(os.cpu_count() or 4, max(1, len(jobs)))) as ex:
         list(ex.map(run, jobs))
+    if ext_new:
+        os.replace(EXT + ".tmp", EXT)
+        jobs.pop()
     if force or jobs or not os.path.exists(OUT):
         cmd = [nvcc, *ARCH, "-shared", "-o", OUT + ".tmp", *objs, "-lcudart"]
         run(cmd)
