@@ -8,6 +8,36 @@
 
 namespace pi {
 
+#ifdef __CUDACC__
+// The kernels of a layer follow each other closely: each is launched so that its
+// CTAs may start while the kernel before it on the stream ends, allows the same
+// to its own successor, and touches memory only after all before it is complete
+// and visible (products of 1024x4096 with one token, one after the other: 4.9 us
+// each instead of 6.2).  allow_next() is for kernels whose CTAs all run at once: where
+// they come in turns, waiting successors would take their places (8 x 4096 rows read:
+// 39.8 us with it, 35.2 without).
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_close(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+#endif
+
 constexpr int kInt4MaxTokens = 32;
 // Packed INT4 matrix: units of 16 rows x 64 columns, unit (row tile, k) at
 // (tile * units_per_row + k) * kInt4Unit.

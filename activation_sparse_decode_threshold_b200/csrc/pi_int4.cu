@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
     const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem + C::kSlots)) + warp * depth * C::kRing;
     float *sums = reinterpret_cast<float *>(smem + C::kSlots + W * C::kRing * depth);
     uint16_t *xs = reinterpret_cast<uint16_t *>(smem + C::fixed(depth, p.tokens));
+    allow_next();
+    after_previous();
     const int cols = p.tokens * PARTS, stride = chunk * 64 + 32;   // 64 bytes past a multiple of 128: no bank conflicts
     const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1), cluster = blockIdx.x >> log_cs;
     const int tiles = (p.n + 15) / 16;
@@ -415,19 +417,9 @@ cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
     if (chunk > units) chunk = units;
     int clusters = cs == 1 ? p.n_sm : p.clusters[cs == 2 ? 0 : cs == 4 ? 1 : 2];
     if (clusters > tiles) clusters = tiles;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(clusters * cs);
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::fixed(depth, p.tokens) + cols * (chunk * 64 + 32) * 2;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cs;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cs > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_matvec<BF, PARTS, NT>, p, cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3, clusters, chunk, depth,
-                              p.tokens < C::kWarps ? C::kWarps / p.tokens : 1);
+    return launch_close(k_matvec<BF, PARTS, NT>, dim3(clusters * cs), C::kThreads, C::fixed(depth, p.tokens) + cols * (chunk * 64 + 32) * 2,
+                        st, cs, p, cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3, clusters, chunk, depth,
+                        p.tokens < C::kWarps ? C::kWarps / p.tokens : 1);
 }
 
 template <bool BF, int PARTS>

@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_append(AppendParams p)
     __shared__ double2 turn[64];
     __shared__ float2 turn_f[64];
     __shared__ double rows[kAppendWarps][D];
+    after_previous();
     const int t = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int pos = p.pos[t], seq = p.seq ? p.seq[t] : t;
     if (pos < 0) return;
@@ -274,6 +275,7 @@ constexpr int kReadWarps = 8;
 template <int FMT, int D>
 __global__ void __launch_bounds__(32 * kReadWarps) k_read(ReadParams p, int block)
 {
+    after_previous();
     const int lane = threadIdx.x % 32, per = p.kv_heads * (D / 8);   // pieces of a token
     const int base = (blockIdx.x * kReadWarps + threadIdx.x / 32) * block;
     long long my_row = -1;
@@ -323,9 +325,7 @@ cudaError_t read_launch(const ReadParams &p, cudaStream_t st)
     int block = (p.tokens + 32 * p.n_sm - 1) / (32 * p.n_sm);
     if (block > 32) block = 32;
     const int grid = (p.tokens + block * kReadWarps - 1) / (block * kReadWarps);
-    if (p.dim == 128) k_read<FMT, 128><<<grid, 32 * kReadWarps, 0, st>>>(p, block);
-    else k_read<FMT, 64><<<grid, 32 * kReadWarps, 0, st>>>(p, block);
-    return cudaGetLastError();
+    return launch_close(p.dim == 128 ? k_read<FMT, 128> : k_read<FMT, 64>, dim3(grid), 32 * kReadWarps, 0, st, 1, p, block);
 }
 
 }  // namespace
@@ -338,9 +338,7 @@ cudaError_t kv_append(const AppendParams &p, cudaStream_t st)
     const int most = (total + kAppendWarps - 1) / kAppendWarps;
     if (split > most) split = most;
     const dim3 grid(p.tokens, split);
-    if (p.dim == 128) k_append<4><<<grid, 32 * kAppendWarps, 0, st>>>(p);
-    else k_append<2><<<grid, 32 * kAppendWarps, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_close(p.dim == 128 ? k_append<4> : k_append<2>, grid, 32 * kAppendWarps, 0, st, 1, p);
 }
 
 cudaError_t kv_read(const ReadParams &p, cudaStream_t st)

@@ -295,6 +295,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     __shared__ float2 joint_of[H];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int n = p.c.n_seqs;
+    allow_next();
+    after_previous();
 
     // ---- units before each thread's block of sequences --------------------
     const int per = (n + T - 1) / T;
@@ -1066,8 +1068,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st, bool set)
     using C = Cfg<FMT, D, NB>;
     if (set) return cudaFuncSetAttribute(k_paged<FMT, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     const int blocks = (p.group + C::kHeads - 1) / C::kHeads;
-    k_paged<FMT, D, NB><<<p.n_sm, 32 * C::kWarps, C::kSmem, st>>>(p, p.kv_heads * blocks, blocks);
-    return cudaGetLastError();
+    return launch_close(k_paged<FMT, D, NB>, dim3(p.n_sm), 32 * C::kWarps, C::kSmem, st, 1, p, p.kv_heads * blocks, blocks);
 }
 
 template <int FMT, int D>
