@@ -319,6 +319,101 @@ cudaError_t append_by_tokens(const AppendParams &p, cudaStream_t st)
     return p.tokens > p.n_sm ? append_launch<D, 8>(p, st, 5) : append_launch<D, 4>(p, st, 4);
 }
 
+// Eight elements of a cache row: what is loaded, and as floats.
+template <int FMT>
+struct Eight {
+    uint4 w;
+    float s;
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, long long row, int D, int at)
+    {
+        const long long i = row * D + at;
+        if (FMT == kI8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(codes + i);
+            w.x = v.x, w.y = v.y;
+            s = reinterpret_cast<const float *>(scales)[row];
+        } else if (FMT == kI4) {
+            w.x = *reinterpret_cast<const uint32_t *>(codes + i / 2);
+            s = __half2float(reinterpret_cast<const __half *>(scales)[i / 32]);
+        } else {
+            w = *reinterpret_cast<const uint4 *>(codes + 2 * i);
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (FMT == kI8) v[e] = s * float(int8_t(u[e / 4] >> (8 * (e & 3))));
+            else if (FMT == kI4) v[e] = s * float(int((u[0] >> (4 * e)) & 15) - 8);
+            else {
+                const float2 f = FMT == kF16 ? __half22float2(*reinterpret_cast<const __half2 *>(&u[e / 2]))
+                                             : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e / 2]));
+                v[e] = e & 1 ? f.y : f.x;
+            }
+        }
+    }
+};
+
+// Bound by the bytes written (for 4 bits to bf16, 8 of 10.25).  A warp takes up
+// to 32 tokens, whose places its lanes look up at once, and moves a token's heads
+// in pieces of 8 elements for each lane, four of K and four of V under way.
+constexpr int kReadWarps = 8;
+template <int FMT, int D>
+__global__ void __launch_bounds__(32 * kReadWarps) k_read(ReadParams p, int block)
+{
+    after_previous();
+    const int lane = threadIdx.x % 32, per = p.kv_heads * (D / 8);   // pieces of a token
+    const int base = (blockIdx.x * kReadWarps + threadIdx.x / 32) * block;
+    long long my_row = -1;
+    if (lane < block && base + lane < p.tokens)
+        my_row = row_of(p.c, p.seq ? p.seq[base + lane] : base + lane, p.pos[base + lane], p.err);
+    for (int b = 0; b < block; ++b) {
+        const long long row0 = __shfl_sync(~0u, my_row, b);
+        if (row0 < 0) continue;
+        const long long out = (long long)(base + b) * per;
+        for (int c0 = lane; c0 < per; c0 += 128) {
+            Eight<FMT> x[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + 32 * i;
+                if (c >= per) break;
+                const long long row = row0 + (long long)(c / (D / 8)) * p.c.head_rows;
+                x[0][i].load(p.c.k, p.c.ks, row, D, c % (D / 8) * 8);
+                x[1][i].load(p.c.v, p.c.vs, row, D, c % (D / 8) * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (c0 + 32 * i >= per) break;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    float v[8];
+                    x[kv][i].values(v);
+                    uint8_t *dst = kv ? p.v : p.k;
+                    const long long j = out + c0 + 32 * i;
+                    if (p.dt == kF32) {
+                        float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(dst) + j * 8);
+                        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(dst + j * 16) = make_uint4(pack2(v[0], v[1], p.dt), pack2(v[2], v[3], p.dt),
+                                                                              pack2(v[4], v[5], p.dt), pack2(v[6], v[7], p.dt));
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int FMT>
+cudaError_t read_launch(const ReadParams &p, cudaStream_t st)
+{
+    // tokens of a warp: so many that each SM has 32 warps of them, 32 at most
+    int block = (p.tokens + 32 * p.n_sm - 1) / (32 * p.n_sm);
+    if (block > 32) block = 32;
+    const int grid = (p.tokens + block * kReadWarps - 1) / (block * kReadWarps);
+    return launch_close(p.dim == 128 ? k_read<FMT, 128> : k_read<FMT, 64>, dim3(grid), 32 * kReadWarps, 0, st, 1, p, block);
+}
+
 }  // namespace
 
 cudaError_t kv_append(const AppendParams &p, cudaStream_t st)
