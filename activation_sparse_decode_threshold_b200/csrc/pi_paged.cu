@@ -262,10 +262,10 @@ struct Cursor {
     Span span;
 };
 
-// An item that has partial results in a CTA: their slots by bit, and the CTAs that hold its first and last chunk.
+// An item that has partial results in a CTA: their slots, and the CTAs that hold its first and last chunk.
 struct Joint {
     int s, item, a, b;
-    unsigned slots;
+    int begin, count;      // in the list of slots
 };
 
 enum { kFirst = 1, kLast = 2, kWhole = 4 };   // a chunk in its segment; a segment that is its whole item
@@ -289,8 +289,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     __shared__ int sums[W], offs[T];
     // partial results: slot 2 w of warp w's first segment (in global memory), 2 w + 1 of its last (in its buffer)
     __shared__ int part_s[kSlots], part_item[kSlots];
-    __shared__ float part_m[2 * W][H], part_l[2 * W][H];
+    __shared__ float part_m[2 * W][H], part_l[2 * W][H], part_f[2 * W][H];
     __shared__ Joint joints[2 * W];
+    __shared__ int slot_list[kSlots];
+    __shared__ const float *slot_at[kSlots];
     __shared__ int n_joints, last[2];
     __shared__ float2 joint_of[H];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     auto place = [](int r, int i) { return r * P + (i ^ (P >= 8 ? r & 7 : P == 4 ? (r >> 1) & 3 : (r >> 2) & 1)); };
     constexpr int RI = 32 / P;            // rows of one copy instruction
     const int my_row = lane / P, my_piece = lane % P;
-    const unsigned slot_bytes = p.c.slot_rows * C::kRow, scale_slot = p.c.slot_rows * C::kScale;   // 2^18 at most
+    const unsigned slot_bytes = p.c.slot_rows * C::kRow;   // 2^18 at most
     // Pages of the 8 positions from 8 (page_g + lane) of sequence page_s.
     int page_s = -1, page_g = 0, my_page = -1;
     int issued = 0;
@@ -388,37 +390,51 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         if (pos + CH > at.span.hi) mask = at.span.hi > pos ? (1u << (at.span.hi - pos)) - 1 : 0;
         if (pos < at.span.lo) mask &= ~((1u << (at.span.lo - pos)) - 1);
         // first rows of the groups of 8; a row without a position is filled with zeros (its memory is not read)
-        long long first_row[2 * R];
+        long long first_row[2 * R], key_row = 0;   // key_row: of position key, whose scales this lane copies
+        const int key = lane % CH;
         const int head = at.item / blocks_per_head * p.c.head_rows;
-#pragma unroll
-        for (int i = 0; i < 2 * R; ++i) {
-            const int page = __shfl_sync(~0u, my_page, grp - page_g + i);
-            if (unsigned(page) >= unsigned(p.c.n_pages)) {
-                if (lane == 0 && (mask >> (8 * i) & 0xffu)) atomicExch(p.err, int(kDevCheck));
-                mask &= ~(0xffu << (8 * i));
-                first_row[i] = 0;
-            } else {
-                first_row[i] = (long long)page * p.c.page_rows + (((pos + 8 * i) & (p.c.page_size - 1)) * p.c.slot_rows + head);
+        auto row_at = [&](int page, int position) -> long long {
+            return unsigned(page) < unsigned(p.c.n_pages)
+                       ? (long long)page * p.c.page_rows + ((position & (p.c.page_size - 1)) * p.c.slot_rows + head) : -1;
+        };
+        if (p.c.page_size >= CH) {   // one page holds them all
+            const long long row = row_at(__shfl_sync(~0u, my_page, grp - page_g + ((__ffs(mask | 1u << (CH - 1)) - 1) >> 3)), pos);
+            if (row < 0) {
+                if (lane == 0 && mask) atomicExch(p.err, int(kDevCheck));
+                mask = 0;
             }
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) first_row[i] = max(row, 0ll) + 8 * i * p.c.slot_rows;
+            if (C::kScale) key_row = max(row, 0ll) + key * p.c.slot_rows;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) {
+                const long long row = row_at(__shfl_sync(~0u, my_page, grp - page_g + i), pos + 8 * i);
+                if (row < 0) {
+                    if (lane == 0 && (mask & 0xffu << (8 * i))) atomicExch(p.err, int(kDevCheck));
+                    mask &= ~(0xffu << (8 * i));
+                }
+                first_row[i] = max(row, 0ll);
+            }
+            if (C::kScale) key_row = max(row_at(__shfl_sync(~0u, my_page, grp - page_g + key / 8), pos + key), 0ll);
         }
         const uint32_t dst = ring_u + stage * C::kStage;
+        const bool all = mask == (CH == 32 ? ~0u : 0xffffu);
 #pragma unroll
         for (int i = 0; i < CH / RI; ++i) {
             const int row = my_row + i * RI;
             const long long off = (RI == 16 && my_row >= 8 ? first_row[i * RI / 8 + 1] : first_row[i * RI / 8]) * C::kRow +
                                   ((row & 7) * slot_bytes + 16 * my_piece);
             const uint32_t to = dst + 16 * place(row, my_piece);
-            copy_async<16>(to, p.c.k + off, (mask >> row) & 1);
-            copy_async<16>(to + C::kOffV, p.c.v + off, (mask >> row) & 1);
+            const bool live = all || (mask >> row) & 1;
+            copy_async<16>(to, p.c.k + off, live);
+            copy_async<16>(to + C::kOffV, p.c.v + off, live);
         }
         if (C::kScale) {   // entries: K of all positions, then V
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int entry = lane + 32 * i, key = entry % CH;
-                long long row = first_row[0];
-#pragma unroll
-                for (int j = 1; j < 2 * R; ++j) row = key / 8 == j ? first_row[j] : row;
-                const uint8_t *base = (entry < CH ? p.c.ks : p.c.vs) + row * C::kScale + (key & 7) * scale_slot;
+                const int entry = lane + 32 * i;
+                const uint8_t *base = (entry < CH ? p.c.ks : p.c.vs) + key_row * C::kScale;
                 copy_async<C::kScale ? C::kScale : 4>(dst + C::kOffS + entry * 8, base, (mask >> key) & 1);
             }
         }
@@ -876,11 +892,17 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     __syncthreads();
 
     // ---- partial results of the CTA's warps, joined for each of their items ---------
+    float *const cta_part = p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W) * (C::kPart / 4);
     if (warp == 0) {   // one lane for each slot: the first slot of an item's run makes its entry
         const int s = part_s[lane], item = s >= 0 ? part_item[lane] : 0;
         const unsigned valid = __ballot_sync(~0u, s >= 0), before = valid & ((1u << lane) - 1);
         const int prev = before ? 31 - __clz(before) : lane;
         const int ps = __shfl_sync(~0u, s, prev), pi = __shfl_sync(~0u, item, prev);
+        if (s >= 0) {
+            slot_list[__popc(before)] = lane;
+            slot_at[__popc(before)] = lane & 1 ? reinterpret_cast<const float *>(smem + W * C::kRing + (lane / 2) * C::kBuf)
+                                               : cta_part + (size_t)(lane / 2) * (C::kPart / 4);
+        }
         const bool head = s >= 0 && (!before || ps != s || pi != item);
         const unsigned heads = __ballot_sync(~0u, head);
         if (head) {
@@ -888,7 +910,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             const unsigned later = heads & ~((2u << lane) - 1);
             j.s = s;
             j.item = item;
-            j.slots = valid & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : ~0u);
+            j.begin = __popc(before);
+            j.count = __popc(valid & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : ~0u));
             int start = offs[s / per];
             for (int r = s / per * per; r < s; ++r) {
                 const Span sp = span_of<CH>(p, r, false);
@@ -904,10 +927,6 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     }
     __syncthreads();
     const int nj = n_joints;
-    auto part_of = [&](int slot) {
-        return slot & 1 ? reinterpret_cast<const float *>(smem + W * C::kRing + (slot / 2) * C::kBuf)
-                        : p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W + slot / 2) * (C::kPart / 4);
-    };
     // this CTA's partial results of items that others share: 2 CTA for one that began before it, 2 CTA + 1 for one
     // that begins in it
     auto far_of = [&](int cta, int a) { return p.part + (size_t)(2 * cta + (cta == a)) * (C::kPart / 4); };
@@ -930,19 +949,19 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         }
         if (p.lse && d == 0) p.lse[(long long)j.s * p.heads + head] = lse_of(jm, jl);
     };
-    // weights of the slots by (item, head) in place of their m; the sums m and l in the rings, which are empty
+    // weights of the slots by (item, head); the sums m and l in the rings, which are empty
     float *joint_m = reinterpret_cast<float *>(smem), *joint_l = joint_m + 2 * W * H;
     for (int e = threadIdx.x; e < nj * H; e += T) {
         const int h = e % H;
-        const unsigned slots = joints[e / H].slots;
+        const int k0 = joints[e / H].begin, k1 = k0 + joints[e / H].count;
         float jm = -FLT_MAX, jl = 0.f;
-#pragma unroll 1
-        for (unsigned k = slots; k; k &= k - 1) jm = fmaxf(jm, part_m[__ffs(k) - 1][h]);
-#pragma unroll 1
-        for (unsigned k = slots; k; k &= k - 1) {
-            const int i = __ffs(k) - 1;
+#pragma unroll 4
+        for (int k = k0; k < k1; ++k) jm = fmaxf(jm, part_m[slot_list[k]][h]);
+#pragma unroll 4
+        for (int k = k0; k < k1; ++k) {
+            const int i = slot_list[k];
             const float f = exp2_(part_m[i][h] - jm);
-            part_m[i][h] = f;
+            part_f[k][h] = f;
             jl += f * part_l[i][h];
         }
         joint_m[e] = jm;
@@ -952,25 +971,21 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 #pragma unroll 1
     for (int e = threadIdx.x; e < nj * H * D / 4; e += T) {
         const Joint &j = joints[e / (H * D / 4)];
-        const int h = e / (D / 4) % H, d = 4 * e % D, first_slot = __ffs(j.slots) - 1;
+        const int h = e / (D / 4) % H, d = 4 * e % D, k1 = j.begin + j.count;
         float4 jo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (unsigned k = j.slots; k;) {   // four slots at a time
+        for (int k = j.begin; k < k1; k += 4) {   // four slots at a time
             float4 v[4];
             float f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int slot = k ? __ffs(k) - 1 : first_slot;
-                v[i] = *reinterpret_cast<const float4 *>(part_of(slot) + h * DP + d);
-                f[i] = part_m[slot][h];
-                if (!k) {
-                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    f[i] = 0.f;
-                }
-                k &= k - 1;
+                const int kk = min(k + i, k1 - 1);
+                v[i] = *reinterpret_cast<const float4 *>(slot_at[kk] + h * DP + d);
+                f[i] = part_f[kk][h];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) jo.x += f[i] * v[i].x, jo.y += f[i] * v[i].y, jo.z += f[i] * v[i].z, jo.w += f[i] * v[i].w;
+            for (int i = 0; i < 4; ++i)
+                if (k + i < k1) jo.x += f[i] * v[i].x, jo.y += f[i] * v[i].y, jo.z += f[i] * v[i].z, jo.w += f[i] * v[i].w;
         }
         const float jm = joint_m[e / (D / 4)], jl = joint_l[e / (D / 4)];
         if (j.a == j.b) {
