@@ -108,6 +108,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     return r;
 }
 
+// 1 / x within 2^-23 of it.
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // d = A B + c
 template <bool BF>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2 b, float c0, float c1, float c2, float c3)
@@ -541,7 +549,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                 const int ex = min(max(__float_as_int(top) >> 23, 16), 253);
                 const float down = pow2_of(254 - ex) * (FMT == kI4 ? 0x1p8f : 1.f);
                 if (part == 0)
-                    extra[4 * b + hl] = pow2_of(ex) * (p.softcap > 0.f ? p.scale : p.scale * 1.4426950408889634f) *
+                    extra[4 * b + hl] = pow2_of(ex) * (p.softcap > 0.f ? p.scale * (2.8853900817779268f / p.softcap) : p.scale * 1.4426950408889634f) *
                                         (FMT == kI4 ? 0x1p16f : 1.f);   // (codes of 4 bits are n 2^-24)
                 float sum = 0.f;
 #pragma unroll
@@ -693,20 +701,35 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     }
                 }
         }
-        bool grows = false;
+        // what the mask leaves out is -infinity; cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap))
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int e = 0; e < 2 * R; ++e) {
-                float &y = x[b][e];
-                y *= factor[b];
-                if (p.softcap > 0.f) {   // cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap))
-                    const float z = exp2_(y * (2.8853900817779268f / p.softcap));
-                    y = (p.softcap - 2.f * p.softcap / (1.f + z)) * 1.4426950408889634f;
+            for (int e = 0; e < 2 * R; ++e) x[b][e] *= factor[b];
+        if (p.softcap > 0.f) {
+            const float cap = p.softcap * 1.4426950408889634f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2 * R; ++e) x[b][e] = fmaf(-2.f * cap, reciprocal(1.f + exp2_(x[b][e])), cap);
+        }
+        if (mask != (CH == 32 ? ~0u : 0xffffu)) {
+#pragma unroll
+            for (int e = 0; e < 2 * R; ++e)
+                if (!((mask >> (g + 8 * e)) & 1)) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) x[b][e] = -INFINITY;
                 }
-                if (!((mask >> (g + 8 * e)) & 1)) y = -INFINITY;
-                grows |= y > m[b];   // (a NaN is passed over here and makes l and o NaN below)
-            }
+        }
+        // (a NaN is passed over by the maxima and makes l and o NaN below)
+        bool grows = false;
+        float top[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            top[b] = fmaxf(x[b][0], x[b][1]);
+            if (R == 2) top[b] = fmaxf(top[b], fmaxf(x[b][2 * R - 2], x[b][2 * R - 1]));
+            grows |= top[b] > m[b];
+        }
         int big = 0;   // exponent of the largest V scale
         if (FMT == kI8) {
             float v = __uint_as_float(vs[0].x);
@@ -741,13 +764,11 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float top = m[b];
-#pragma unroll
-                for (int e = 0; e < 2 * R; ++e) top = fmaxf(top, x[b][e]);
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-                const float shrink = exp2_(m[b] - top), f = shrink * both;
+                float y = fmaxf(top[b], m[b]);
+                y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
+                y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
+                y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+                const float shrink = exp2_(m[b] - y), f = shrink * both;
                 l[b] *= shrink;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
@@ -756,7 +777,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     acc[b][i][2] *= f;
                     acc[b][i][3] *= f;
                 }
-                m[b] = top;
+                m[b] = y;
             }
         }
         // ---- weights
