@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 
     Cursor at{};
     if (left > 0) {
-        int b = 0, end = T;   // the block that holds unit u0: the last one that starts at or before it
+        int b = 0, end = min(T, n);   // the block that holds unit u0: the last one that starts at or before it
         while (end - b > 1) {
             const int mid = (b + end) / 2;
             if (offs[mid] <= u0) b = mid;
@@ -507,6 +507,14 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             uint32_t *words = reinterpret_cast<uint32_t *>(buf);
             float *extra = buf + H * DP;   // factors, then biases
             const int hl = lane / 8, part = lane % 8;
+            if (NB > 1) {   // all on their way to L1 at once
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int head = min(cur_item % blocks_per_head * H + 4 * b + hl, p.group - 1);
+                    const long long at_q = cur_s * p.qs + (long long)(cur_item / blocks_per_head * p.group + head) * D + part * (D / 8);
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + at_q * (p.dt == kF32 ? 4 : 2)));
+                }
+            }
 #pragma unroll 1
             for (int b = 0; b < NB; ++b) {
                 constexpr int E = D / 8;   // elements of a lane: part E, ...
