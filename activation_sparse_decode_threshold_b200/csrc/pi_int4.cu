@@ -130,6 +130,17 @@ __device__ __forceinline__ float peer(const float *p, int rank)
 // numbers, each the leading 8 bits of what is left (cut off, so that no part
 // overflows; 24 bits in all).  An infinity or NaN stays in the first part.
 __device__ __forceinline__ float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+// Of eight numbers, some not finite: their leading parts (part 0; a NaN's digits
+// may all be among the others), or what is left of the finite ones.
+__device__ __forceinline__ void first_part_only(const float (&v)[8], int part, uint32_t (&u)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // (inf - inf and NaN - NaN leave NaN: nothing is left of these)
+        const uint32_t b = isnan(v[e]) ? (part == 0 ? 0x7fc0u : 0u) : __float_as_uint(v[e]) >> 16;
+        u[e / 2] = e & 1 ? u[e / 2] | (b << 16) : b;
+    }
+}
 
 __device__ __forceinline__ float value_of(const uint8_t *p, long long i, int dt)
 {
@@ -175,7 +186,6 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
     float *sums = reinterpret_cast<float *>(smem + C::kSlots + W * C::kRing * depth);
     uint16_t *xs = reinterpret_cast<uint16_t *>(smem + C::fixed(depth, p.tokens));
     allow_next();
-    after_previous();
     const int cols = p.tokens * PARTS, stride = chunk * 64 + 32;   // 64 bytes past a multiple of 128: no bank conflicts
     const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1), cluster = blockIdx.x >> log_cs;
     const int tiles = (p.n + 15) / 16;
@@ -223,6 +233,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                 if (first + ks - k <= end) to_warp[tile] = warp;
                 if (last && first + 2 * ks - k <= end) to_warp[tile + 1] = warp;
             }
+            after_previous();   // (the matrix is there since its creation; x and y may be the work of kernels before)
             if (t0 == t_begin || !one_pass) {
                 // a warp for each token, or for each of `split` parts of it; the squares on the way
                 const int pieces = ks * 8;   // of 8 columns
@@ -255,17 +266,19 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
                             }
+                            float odd = 0.f;   // NaN if any is not finite
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) odd = fmaf(v[e], 0.f, odd);
 #pragma unroll
                             for (int part = 0; part < PARTS; ++part) {
                                 uint32_t u[4];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float cutoff = cut(v[e]);
-                                    const uint32_t b = isnan(v[e]) ? 0x7fc0u : __float_as_uint(v[e]) >> 16;
-                                    u[e / 2] = e & 1 ? u[e / 2] | (b << 16) : b;
-                                    v[e] = isfinite(v[e]) ? v[e] - cutoff : 0.f;
-                                }
+                                for (int e = 0; e < 4; ++e)
+                                    u[e] = __byte_perm(__float_as_uint(v[2 * e]), __float_as_uint(v[2 * e + 1]), 0x7632);
+                                if (odd != 0.f) first_part_only(v, part, u);
                                 *reinterpret_cast<uint4 *>(row + part * p.tokens * stride + 8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[e] -= cut(v[e]);
                             }
                         }
                     }
