@@ -308,31 +308,37 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     allow_next();
     after_previous();
 
-    // ---- units before each thread's block of sequences --------------------
-    const int per = (n + T - 1) / T;
-    int mine = 0;
+    // ---- units before each sequence, or each thread's block of `per` sequences ---------
+    const bool few = n <= 32;   // every warp counts for itself (and needs no barrier)
+    const int per = few ? 1 : (n + T - 1) / T;
+    int mine = 0, total = 0, scan;
 #pragma unroll 1
-    for (int s = threadIdx.x * per; s < min(n, (int(threadIdx.x) + 1) * per); ++s) {
-        const Span r = span_of<CH>(p, s, blockIdx.x == 0);
+    for (int i = few ? lane : threadIdx.x * per, end = min(n, i + per); i < end; ++i) {
+        const Span r = span_of<CH>(p, i, blockIdx.x == 0 && (!few || warp == 0));
         mine += (r.c1 - r.c0 + kStart) * items;
     }
-    int scan = mine;
+    scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(~0u, scan, o);
         if (lane >= o) scan += v;
     }
-    if (lane == 31) sums[warp] = scan;
-    if (threadIdx.x < kSlots) part_s[threadIdx.x] = -1;
-    __syncthreads();
-    int total = 0, before = 0;
+    if (lane < 2) part_s[2 * warp + lane] = -1;
+    if (few) {
+        total = __shfl_sync(~0u, scan, 31);
+        if (warp == 0) offs[lane] = scan - mine;   // (for the joins)
+    } else {
+        if (lane == 31) sums[warp] = scan;
+        __syncthreads();
+        int before = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        before += w < warp ? sums[w] : 0;
-        total += sums[w];
+        for (int w = 0; w < W; ++w) {
+            before += w < warp ? sums[w] : 0;
+            total += sums[w];
+        }
+        offs[threadIdx.x] = before + scan - mine;   // (blocks without sequences: the total)
+        __syncthreads();
     }
-    offs[threadIdx.x] = before + scan - mine;   // (blocks without sequences: the total)
-    __syncthreads();
 
     // ---- this warp's share ---------------------------------------------------
     int ctas = min((total + W - 1) / W, int(gridDim.x));   // at least a unit for each warp
@@ -348,14 +354,20 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 
     Cursor at{};
     if (left > 0) {
-        int b = 0, end = min(T, n);   // the block that holds unit u0: the last one that starts at or before it
-        while (end - b > 1) {
-            const int mid = (b + end) / 2;
-            if (offs[mid] <= u0) b = mid;
-            else end = mid;
+        int b = 0;   // the block that holds unit u0: the last one that starts at or before it
+        int rest;
+        if (few) {
+            b = __popc(__ballot_sync(~0u, lane < n && scan - mine <= u0)) - 1;
+            rest = u0 - __shfl_sync(~0u, scan - mine, b);
+        } else {
+            for (int end = T; end - b > 1;) {
+                const int mid = (b + end) / 2;
+                if (offs[mid] <= u0) b = mid;
+                else end = mid;
+            }
+            rest = u0 - offs[b];
         }
         at.s = b * per;
-        int rest = u0 - offs[b];
         for (;;) {
             at.span = span_of<CH>(p, at.s, false);
             const int here = (at.span.c1 - at.span.c0 + kStart) * items;
@@ -378,7 +390,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     const unsigned slot_bytes = p.c.slot_rows * C::kRow;   // 2^18 at most
     // Pages of the 8 positions from 8 (page_g + lane) of sequence page_s.
     int page_s = -1, page_g = 0, my_page = -1;
-    int issued = 0;
+    int issued = 0, head = at.item / blocks_per_head * p.c.head_rows;
     bool first = true, from_start = at.c == at.span.c0;
     auto issue = [&](int stage) {
         if (left <= 0) {
@@ -400,7 +412,6 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         // first rows of the groups of 8; a row without a position is filled with zeros (its memory is not read)
         long long first_row[2 * R], key_row = 0;   // key_row: of position key, whose scales this lane copies
         const int key = lane % CH;
-        const int head = at.item / blocks_per_head * p.c.head_rows;
         auto row_at = [&](int page, int position) -> long long {
             return unsigned(page) < unsigned(p.c.n_pages)
                        ? (long long)page * p.c.page_rows + ((position & (p.c.page_size - 1)) * p.c.slot_rows + head) : -1;
@@ -467,6 +478,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             at.span = span_of<CH>(p, at.s, false);
         }
         at.c = at.span.c0;
+        head = at.item / blocks_per_head * p.c.head_rows;
     };
     // ---- one chunk after the other ---------------------------------------------
     uint2 q[C::kQShared ? 1 : KS][C::kQShared ? 1 : NB];
@@ -923,7 +935,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     // ---- partial results of the CTA's warps, joined for each of their items ---------
     float *const cta_part = p.part + (size_t)gridDim.x * 2 * (C::kPart / 4) + (size_t)(blockIdx.x * W) * (C::kPart / 4);
     if (warp == 0) {   // one lane for each slot: the first slot of an item's run makes its entry
-        const int s = part_s[lane], item = s >= 0 ? part_item[lane] : 0;
+        const int s = lane < 2 * W ? part_s[lane] : -1, item = s >= 0 ? part_item[lane] : 0;
         const unsigned valid = __ballot_sync(~0u, s >= 0), before = valid & ((1u << lane) - 1);
         const int prev = before ? 31 - __clz(before) : lane;
         const int ps = __shfl_sync(~0u, s, prev), pi = __shfl_sync(~0u, item, prev);
@@ -941,16 +953,17 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             j.item = item;
             j.begin = __popc(before);
             j.count = __popc(valid & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : ~0u));
-            int start = offs[s / per];
-            for (int r = s / per * per; r < s; ++r) {
+            int start = offs[few ? s : s / per];
+            for (int r = few ? s : s / per * per; r < s; ++r) {
                 const Span sp = span_of<CH>(p, r, false);
                 start += (sp.c1 - sp.c0 + kStart) * items;
             }
             const Span sp = span_of<CH>(p, s, false);
             const int nc = sp.c1 - sp.c0;
             start += item * (nc + kStart) + kStart;
-            j.a = shares.of(start);   // CTAs of its first and last chunk
-            j.b = shares.of(start + nc - 1);
+            j.a = j.b = blockIdx.x;   // CTAs of its first and last chunk
+            if (start < cta0) j.a = shares.of(start);
+            if (start + nc > cta0 + units) j.b = shares.of(start + nc - 1);
         }
         if (lane == 0) n_joints = __popc(heads);
     }
