@@ -14,7 +14,6 @@ namespace pi {
 namespace {
 
 constexpr int kMaxCluster = 8;
-constexpr int kShareX = 112 * 1024;     // a CTA's part of x above this: the columns are split over more CTAs
 
 // Unit (row tile, 64 columns): lane (g = lane / 4, t = lane % 4) finds at 16 lane
 // the eight columns 8t .. 8t+7 of rows g and g + 8, first of the unit's first
@@ -156,10 +155,11 @@ struct MvCfg {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBatch = 4;                                // units that a warp takes from its ring at once
     static constexpr int kSlot = 16 * 8 * NT;                       // sums of a warp for one row tile
-    // Bytes: slots; rings of `depth` batches; sums of a CTA's row tiles, [tile][token][row]; behind them the chunk of x.
-    static constexpr int kSlots = 2 * kWarps * kSlot * 4, kRing = kBatch * kInt4Unit, kSum = kWarps * 16 * 4;
+    // Bytes: a slot for each warp's first tile (its second's takes the place of its ring); rings of `depth` batches; sums of a CTA's row tiles, [tile][token][row]; behind them the chunk of x.
+    static constexpr int kSlots = kWarps * kSlot * 4, kRing = kBatch * kInt4Unit, kSum = kWarps * 16 * 4;
     static constexpr int fixed(int depth, int tokens) { return kSlots + kWarps * kRing * depth + kSum * tokens; }
     static constexpr int kRoom = 222 * 1024;
+    static constexpr int kLeastDepth = kSlot * 4 > 2 * kRing ? 3 : 2;
 };
 
 // A cluster takes row tiles (of 16), up to kWarps at a time; its CTAs share the
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
     float *slots = reinterpret_cast<float *>(smem);
     const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem + C::kSlots)) + warp * depth * C::kRing;
+    auto ring_slot = [&](int w) { return reinterpret_cast<float *>(smem + C::kSlots + w * depth * C::kRing); };
     float *sums = reinterpret_cast<float *>(smem + C::kSlots + W * C::kRing * depth);
     uint16_t *xs = reinterpret_cast<uint16_t *>(smem + C::fixed(depth, p.tokens));
     allow_next();
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
 #pragma unroll
                     for (int n8 = 0; n8 < NT; ++n8) xb[n8] += have * 64;
                 }
-                float *slot = slots + (2 * warp + seg) * C::kSlot;
+                float *slot = seg ? ring_slot(warp) : slots + warp * C::kSlot;
 #pragma unroll
                 for (int n8 = 0; n8 < NT; ++n8) {
                     *reinterpret_cast<float2 *>(slot + g * 8 * NT + n8 * 8 + 2 * t4) = make_float2(acc[n8][0], acc[n8][1]);
@@ -361,12 +362,12 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                 for (int t = lane / 16; t < p.tokens; t += 2) {
                     float *sum = sums + (warp * p.tokens + t) * 16 + r;
                     float y = k0 == k_begin ? 0.f : *sum;
-                    const float *src = slots + from * C::kSlot + r * 8 * NT + t;
+                    const float *src = (from & 1 ? ring_slot(from / 2) : slots + from / 2 * C::kSlot) + r * 8 * NT + t;
 #pragma unroll
                     for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
-                    src = slots + (from / 2 + 1) * 2 * C::kSlot + r * 8 * NT + t;
+                    src = slots + (from / 2 + 1) * C::kSlot + r * 8 * NT + t;
 #pragma unroll 4
-                    for (int w = 0; w < more; ++w, src += 2 * C::kSlot) {
+                    for (int w = 0; w < more; ++w, src += C::kSlot) {
 #pragma unroll
                         for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
                     }
@@ -417,15 +418,17 @@ template <bool BF, int PARTS, int NT>
 cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
 {
     using C = MvCfg<NT>;
-    static_assert((C::kRoom - C::fixed(2, kInt4MaxTokens)) / (8 * NT) >= 64 + 4 * 128, "a chunk of x has 4 units at least");
+    static_assert((C::kRoom - C::fixed(C::kLeastDepth, kInt4MaxTokens)) / (8 * NT) >= 64 + 4 * 128, "a chunk of x has 4 units at least");
     if (set) return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRoom);
     const int cols = p.tokens * PARTS, tiles = (p.n + 15) / 16;
-    int cs = 1;
-    while (cs < kMaxCluster && cols * (p.ku / cs) * 128 > kShareX && p.ku / cs >= 2) cs *= 2;
-    // the deepest rings that leave room for x's columns at once, or else for a part of them
+    // Over how many CTAs the columns are split: so many that x's part fits into shared memory at once (13 tokens of 8192
+    // columns: two), beside rings as deep as then there is room for; for a CTA of its own three batches deep (8 tokens
+    // of 8192 columns: one CTA with two batches 15.1 us, two CTAs 14.0).
+    auto fits = [&](int cs, int depth) { return C::fixed(depth, p.tokens) + cols * ((p.ku + cs - 1) / cs * 128 + 64) <= C::kRoom; };
+    int cs = 1, depth = 4;
+    while (cs < kMaxCluster && !fits(cs, cs == 1 ? 3 : C::kLeastDepth) && p.ku / cs >= 2) cs *= 2;
+    while (depth > C::kLeastDepth && !fits(cs, depth)) --depth;
     const int units = (p.ku + cs - 1) / cs;
-    int depth = 4;
-    while (depth > 2 && C::fixed(depth, p.tokens) + cols * (units * 128 + 64) > C::kRoom) --depth;
     int chunk = ((C::kRoom - C::fixed(depth, p.tokens)) / cols - 64) / 128;
     if (chunk > units) chunk = units;
     int clusters = cs == 1 ? p.n_sm : p.clusters[cs == 2 ? 0 : cs == 4 ? 1 : 2];
