@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function here has the name of the C entry
 point it calls, turns torch tensors into device/host pointers, and raises
-``PiError`` on a non-OK status.  Every step of the sparse FFN runs in the
+``PiError`` on a non-OK status (the calls of the attention half do so in C++,
+csrc/pi_torch.cpp).  Every step of the sparse FFN runs in the
 library's CUDA kernels; nothing here computes.  Loading fails loudly when the
 library has not been built.
 """

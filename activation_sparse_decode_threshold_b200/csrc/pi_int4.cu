@@ -155,7 +155,8 @@ struct MvCfg {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBatch = 4;                                // units that a warp takes from its ring at once
     static constexpr int kSlot = 16 * 8 * NT;                       // sums of a warp for one row tile
-    // Bytes: a slot for each warp's first tile (its second's takes the place of its ring); rings of `depth` batches; sums of a CTA's row tiles, [tile][token][row]; behind them the chunk of x.
+    // Bytes: a slot for each warp's first tile (its second's takes the place of its ring); rings of `depth` batches; sums
+    // of a CTA's row tiles, [tile][token][row]; behind them the chunk of x.
     static constexpr int kSlots = kWarps * kSlot * 4, kRing = kBatch * kInt4Unit, kSum = kWarps * 16 * 4;
     static constexpr int fixed(int depth, int tokens) { return kSlots + kWarps * kRing * depth + kSum * tokens; }
     static constexpr int kRoom = 222 * 1024;
@@ -167,9 +168,12 @@ struct MvCfg {
 // shared out evenly over its warps, so that a warp has parts of two tiles at
 // most: the sums of these go to two slots in shared memory, from there in order
 // to the tile's sums, and from the CTAs, in order, to y.  Bound by the matrix's
-// bytes: each warp keeps two or three batches of 4 units of 576 bytes under way, and x
-// is brought to each CTA once (for 13 tokens of 8192 columns it is 213 KB, more
-// than the CTA's share of the matrix: hence the clusters).
+// bytes, and before that, as it stands, by the instructions that unpack them (about
+// 110 for a unit of 576 bytes with one tile of tokens): so each warp has few of
+// them beside, keeps two or three batches of 4 units under way, and x is brought to
+// each CTA once (for 13 tokens of 8192 columns it is 213 KB, about as much as the
+// CTA's share of the matrix: hence the clusters).  6144x4096, one fp32 token with
+// its norm: 6.9 us (2.05 TB/s); 8192x8192, 13 tokens: 17.5 us (2.2 TB/s).
 // PARTS: 3 for F32 x, else 1.  NT: tiles of 8 columns of B (tokens * PARTS).
 template <bool BF, int PARTS, int NT>
 __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p, int log_cs, int clusters, int chunk, int depth, int split)

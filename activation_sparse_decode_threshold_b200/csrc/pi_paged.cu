@@ -16,6 +16,12 @@
 // the cache's 16-, 8- or 4-bit numbers, which are exact.  A head's two columns
 // meet in one lane.  Scales of quantised rows are applied in fp32, to the scores
 // (K) and to the weights (V).
+//
+// Measured: 32 ragged texts of bf16 (525 MB) 103 us, 5.1 TB/s; 32768 positions of
+// 4 bits 23.9 us, of which 12 are its chunks' instructions and 10 the way to the
+// first product and from the last to the result; 16 texts of 8 bits in a window,
+// 16 queries to a cached head, 36.8 us, bound by instructions.  Taking 8 instead
+// of 16 heads at a time, with 12 instead of 8 warps, made the last 39.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,7 +32,9 @@
 namespace pi {
 namespace {
 
-constexpr int kStart = 2;             // what the start of an item costs, in chunks
+// What the start of an item costs, in chunks (8-bit window of 16 ragged texts: 1 44.6 us, 2 37.7, 4 37.2; 200 positions:
+// 8.5, 8.4, 10.7).
+constexpr int kStart = 2;
 constexpr int kSlots = 32;            // partial results of a CTA's warps, at most (2 for each)
 
 // FMT: the cache's format.  NB: tiles of 4 query heads that share a cached head.

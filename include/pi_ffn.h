@@ -388,8 +388,9 @@ PI_API void pi_int4_destroy(pi_int4_t m);
  *   add_dev  NULL, or rows like y's (may be y_dev itself: y += W f(x))
  *   y_dev    n_tokens rows of n_rows values [y_dtype], y_stride elements apart
  * Types F32, F16 or BF16.  Products are exact (x in parts that hold all its
- * bits), sums are fp32, y is rounded once.  Each token's row depends on that
- * token alone, the result is deterministic, and calls on several streams may
+ * bits), sums are fp32, y is rounded once.  Each token's row comes from that
+ * token alone (the order of its sums, and so its last bits, may differ with
+ * n_tokens), the result is deterministic, and calls on several streams may
  * overlap.  x must not overlap y, nor add overlap y unless both are the same
  * rows.  Errors: PI_ERR_INVALID_ARG, PI_ERR_CUDA. */
 PI_API pi_status pi_int4_matvec(pi_int4_t m, int n_tokens, pi_dtype x_dtype, const void *x_dev, int64_t x_stride,
