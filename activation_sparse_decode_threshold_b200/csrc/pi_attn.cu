@@ -234,7 +234,8 @@ pi_status pi_attn_create(const pi_attn_desc *desc, pi_attn_t *out)
         return fail(PI_ERR_INVALID_ARG, "rope_theta must be > 0");
     if (!(D.norm_eps >= 0.f) || !std::isfinite(D.norm_eps)) return fail(PI_ERR_INVALID_ARG, "norm_eps must be >= 0");
     if (!std::isfinite(D.scale)) return fail(PI_ERR_INVALID_ARG, "scale must be finite");
-    if (!(D.softcap >= 0.f) || !std::isfinite(D.softcap)) return fail(PI_ERR_INVALID_ARG, "softcap must be >= 0");
+    if (!(D.softcap == 0.f || (D.softcap >= 1e-6f && D.softcap <= 1e6f)))
+        return fail(PI_ERR_INVALID_ARG, "softcap must be 0 or in [1e-6, 1e6]");
     if (D.window < 0) return fail(PI_ERR_INVALID_ARG, "window must be >= 0");
     int n_sm = 0;
     const pi_status st = check_device(D.device, &n_sm);

@@ -116,6 +116,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     return r;
 }
 
+constexpr float kLargeCap = 64.f;
+// cap * tanh(y / cap) for x = 2 log2 e * y / cap.
+__device__ __noinline__ float large_cap(float x, float cap) { return cap * tanhf(0.34657359f * x); }
+
 // 1 / x within 2^-23 of it.
 __device__ __forceinline__ float reciprocal(float x)
 {
@@ -729,7 +733,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     }
                 }
         }
-        // what the mask leaves out is -infinity; cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap))
+        // what the mask leaves out is -infinity; cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap)), which is off by
+        // cap 2^-21 at most: for large caps, whose scores are small beside them, tanh itself
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -739,7 +744,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int e = 0; e < 2 * R; ++e) x[b][e] = fmaf(-2.f * cap, reciprocal(1.f + exp2_(x[b][e])), cap);
+                for (int e = 0; e < 2 * R; ++e)
+                    x[b][e] = p.softcap > kLargeCap ? large_cap(x[b][e], cap) : fmaf(-2.f * cap, reciprocal(1.f + exp2_(x[b][e])), cap);
         }
         if (mask != (CH == 32 ? ~0u : 0xffffu)) {
 #pragma unroll

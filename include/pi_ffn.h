@@ -398,7 +398,7 @@ PI_API pi_status pi_int4_matvec(pi_int4_t m, int n_tokens, pi_dtype x_dtype, con
                                 float norm_eps, void *stream);
 
 /* Heads, cache format and constants shared by an attention layer's calls (one
- * handle serves all layers of the same shape). */
+ * handle serves all layers of the same shape, and owns 6 to 24 MB of scratch). */
 typedef enum { PI_KV_HND = 0, PI_KV_NHD = 1 } pi_kv_layout;
 typedef struct {
     int n_heads;           /* query heads, a multiple of n_kv_heads; <= 1024 */
@@ -412,7 +412,7 @@ typedef struct {
     float rope_theta;      /* pair i turns by position * rope_theta^(-2i/rotary_dim); > 0 if rotated */
     float norm_eps;        /* > 0: q and k heads are normed before the rotation; 0: not */
     float scale;           /* score factor; 0 = 1 / sqrt(head_dim) */
-    float softcap;         /* > 0: score s becomes softcap * tanh(s / softcap); 0: not */
+    float softcap;         /* 1e-6 .. 1e6: score s becomes softcap * tanh(s / softcap); 0: not */
     int window;            /* > 0: a position sees itself and the window - 1 positions before it; 0: all */
     int device;
 } pi_attn_desc;

@@ -238,6 +238,24 @@ def test_attention_an_infinite_scale_spoils_its_group_only(made):
             check(out[s][:, keep], want[:, keep], bound[:, keep] + R.half_step(want[:, keep], torch.float32))
 
 
+@pytest.mark.parametrize("cap", [1e-6, 0.5, 30.0, 64.0, 65.0, 1000.0, 1e6])
+def test_capped_scores_of_all_sizes(made, cap):
+    """One position: the log of the sum is its capped score.  Up to 64 the cap's formula is off by cap 2^-21, above it the
+    score by a few of its own roundings (tanh 2 units of 2^-23, five products of 2^-24, products of 22 bits and their sum
+    of 64 in 24)."""
+    lens = [1, 1, 1]
+    c = R.Cache(gen(31), lens, 1, 64, "f16", 8).cuda()
+    for size in (0.01, 1.0, 40.0):
+        q = size * torch.randn(3, 4, 64, generator=gen(32))
+        a, q, out, lse = attend(made, c, lens, 4, "f32", q=q, softcap=cap)
+        for s in range(3):
+            k = c.rows("k", s, 0, 1)[0, 0]
+            x = (q[s].double() @ k) / 8
+            noise = (q[s].double().abs() @ k.abs()) / 8 * (2.0 ** -21 + 136 * R.U)
+            want = cap * torch.tanh(x / cap)
+            check(lse[s], want, noise + want.abs() * (2.0 ** -21 + 8 * R.U) + (cap * 2.0 ** -21 if cap <= 64 else 0.0), f"cap {cap} size {size}")
+
+
 def test_sequences_that_share_pages(made):
     """A prefix in the pages of two sequences, read by both."""
     c = R.Cache(gen(23), [64, 64], 2, 64, "bf16", 16)
@@ -289,4 +307,11 @@ def test_refused_sizes(made):
     with pytest.raises(B.PiError) as e:
         B.pi_paged_attention(a, cache_of(c), tall, n.expand(65536).contiguous(), q.expand(65536, 1, 64).contiguous(),
                              o.expand(65536, 1, 64).contiguous())
+    assert e.value.status == B.PI_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("cap", [1e-7, 1e7, -INF])
+def test_caps_out_of_range_are_refused(cap):
+    with pytest.raises(B.PiError) as e:
+        B.pi_attn_create(4, 2, 64, softcap=cap)
     assert e.value.status == B.PI_ERR_INVALID_ARG
