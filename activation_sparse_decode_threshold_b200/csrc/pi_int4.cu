@@ -154,7 +154,8 @@ struct MvCfg {
     static constexpr int kWarps = NT <= 4 ? 16 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBatch = 4;                                // units that a warp takes from its ring at once
-    static constexpr int kSlot = 16 * 8 * NT;                       // sums of a warp for one row tile
+    static constexpr int kSlotRow = 8 * NT + 2;                     // (2: rows' same columns meet no bank twice)
+    static constexpr int kSlot = 16 * kSlotRow;                     // sums of a warp for one row tile
     // Bytes: a slot for each warp's first tile (its second's takes the place of its ring); rings of `depth` batches; sums
     // of a CTA's row tiles, [tile][token][row]; behind them the chunk of x.
     static constexpr int kSlots = kWarps * kSlot * 4, kRing = kBatch * kInt4Unit, kSum = kWarps * 16 * 4;
@@ -353,8 +354,8 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                 float *slot = seg ? ring_slot(warp) : slots + warp * C::kSlot;
 #pragma unroll
                 for (int n8 = 0; n8 < NT; ++n8) {
-                    *reinterpret_cast<float2 *>(slot + g * 8 * NT + n8 * 8 + 2 * t4) = make_float2(acc[n8][0], acc[n8][1]);
-                    *reinterpret_cast<float2 *>(slot + (g + 8) * 8 * NT + n8 * 8 + 2 * t4) = make_float2(acc[n8][2], acc[n8][3]);
+                    *reinterpret_cast<float2 *>(slot + g * C::kSlotRow + n8 * 8 + 2 * t4) = make_float2(acc[n8][0], acc[n8][1]);
+                    *reinterpret_cast<float2 *>(slot + (g + 8) * C::kSlotRow + n8 * 8 + 2 * t4) = make_float2(acc[n8][2], acc[n8][3]);
                     acc[n8][0] = acc[n8][1] = acc[n8][2] = acc[n8][3] = 0.f;
                     xb[n8] -= ks * 64;   // (the second tile starts at the first column)
                 }
@@ -366,10 +367,10 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                 for (int t = lane / 16; t < p.tokens; t += 2) {
                     float *sum = sums + (warp * p.tokens + t) * 16 + r;
                     float y = k0 == k_begin ? 0.f : *sum;
-                    const float *src = (from & 1 ? ring_slot(from / 2) : slots + from / 2 * C::kSlot) + r * 8 * NT + t;
+                    const float *src = (from & 1 ? ring_slot(from / 2) : slots + from / 2 * C::kSlot) + r * C::kSlotRow + t;
 #pragma unroll
                     for (int part = PARTS - 1; part >= 0; --part) y += src[part * p.tokens];
-                    src = slots + (from / 2 + 1) * C::kSlot + r * 8 * NT + t;
+                    src = slots + (from / 2 + 1) * C::kSlot + r * C::kSlotRow + t;
 #pragma unroll 4
                     for (int w = 0; w < more; ++w, src += C::kSlot) {
 #pragma unroll

@@ -185,9 +185,12 @@ __device__ __forceinline__ void store_row(const CacheView &c, uint8_t *codes, ui
 __device__ __forceinline__ float root_inv(float x) { return rsqrtf(x); }   // (off by 2 units of 2^-23 at most)
 __device__ __forceinline__ double root_inv(double x) { return rsqrt(x); }
 
-// Places in a vector's row of shared memory: one more after each 8, so that lanes
-// with 8 elements each meet no bank twice.
+// Places in a vector's row of shared memory: more after each 8, so that lanes with
+// 8 elements each meet no bank twice (512 tokens into 4 bits: 9.8 us, without 12.2).
 __device__ __forceinline__ int spread(int i) { return i + (i >> 3); }
+// The same for cosines and sines: whole 16 bytes.
+__device__ __forceinline__ int spread(int i, float2) { return i + 2 * (i >> 3); }
+__device__ __forceinline__ int spread(int i, double2) { return i + (i >> 3); }
 
 // Norm and rotation of elements [at, at + N) of a vector, its other lanes side by
 // side; float for queries, double for keys.  turn: cosine and sine of each
@@ -213,7 +216,7 @@ __device__ __forceinline__ void norm_rotate(const AppendParams &p, const float (
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const T2 a = turn[at + e];
+        const T2 a = turn[spread(at + e, T2())];
         const T y = x[e] * a.x + buf[other[e]] * a.y;
         x[e] = at + e < p.rotary ? y : x[e];
     }
@@ -227,13 +230,13 @@ constexpr int kAppendWarps = 4;
 // tokens, and by instructions (a vector of 128 keys, in 64 bits, takes a warp
 // some 300) where there are many; loads are under way before the angles, and each
 // later one before its turn.  32 + 2 x 8 heads of 128 into 4 bits: one token 3.5
-// us, 512 tokens 12.4 us.
+// us, 512 tokens 9.8 us.
 template <int D, int N, int DT>
 __global__ void __launch_bounds__(32 * kAppendWarps) k_append(AppendParams p)
 {
     constexpr int L = D / N, V = 32 / L, W = kAppendWarps;   // lanes of a vector, vectors of a warp
-    __shared__ double2 turn[D];
-    __shared__ float2 turn_f[D];
+    __shared__ double2 turn[D + D / 8];
+    __shared__ __align__(16) float2 turn_f[D + D / 4];
     __shared__ double rows[W][V][D + D / 8];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, at = lane % L * N, mine = lane / L;
     after_previous();
@@ -262,10 +265,20 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_append(AppendParams p)
         double s, c;
         sincos(double(pos) * p.freq[i], &s, &c);
         const int a = p.pairs ? 2 * i : i, b = p.pairs ? 2 * i + 1 : i + half;
-        turn[a] = make_double2(c, -s);
-        turn[b] = make_double2(c, s);
-        turn_f[a] = make_float2(float(c), float(-s));
-        turn_f[b] = make_float2(float(c), float(s));
+        turn[spread(a, double2())] = make_double2(c, -s);
+        turn[spread(b, double2())] = make_double2(c, s);
+        turn_f[spread(a, float2())] = make_float2(float(c), float(-s));
+        turn_f[spread(b, float2())] = make_float2(float(c), float(s));
+    }
+    // V needs no angles
+#pragma unroll 1
+    for (; j < kv_tasks && row0 >= 0; j += step) {
+        float next[N] = {};
+        if (j + step < tasks) load(j + step, next);
+        const int h = head_of(j);
+        store_row<D, N>(p.c, p.c.v, p.c.vs, row0 + (long long)h * p.c.head_rows, at, h < p.kv_heads, f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = next[e];
     }
     __syncthreads();
     if (row0 < 0) return;
@@ -285,14 +298,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_append(AppendParams p)
             if (h < p.heads) store_vals<N>(p.q_out, t * p.os + h * D + at, DT, f);
         } else {
             const long long row = row0 + (long long)h * p.c.head_rows;
-            if (j >= kv_tasks && (p.rotary || p.eps > 0.f)) {
+            if (p.rotary || p.eps > 0.f) {
                 double x[N];
 #pragma unroll
                 for (int e = 0; e < N; ++e) x[e] = f[e];
                 norm_rotate<D, N, double>(p, kw, turn, other, rows[warp][mine], at, x);
                 store_row<D, N>(p.c, p.c.k, p.c.ks, row, at, h < p.kv_heads, x);
             } else {
-                store_row<D, N>(p.c, j < kv_tasks ? p.c.v : p.c.k, j < kv_tasks ? p.c.vs : p.c.ks, row, at, h < p.kv_heads, f);
+                store_row<D, N>(p.c, p.c.k, p.c.ks, row, at, h < p.kv_heads, f);
             }
         }
 #pragma unroll
@@ -313,7 +326,7 @@ cudaError_t append_launch(const AppendParams &p, cudaStream_t st, int ctas)
 }
 
 // Few tokens: 4 elements to a lane, the shorter way (one token of 32 + 2 x 8 heads of 128 into 4 bits: 3.5 us, with 8
-// elements 4.3).  Many: 8, in fewer instructions (512 tokens 12.4 us, with 4 elements 14.0).  Both are even at 150 to 200.
+// elements 4.3).  Many: 8, in fewer instructions (512 tokens 9.9 us, with 4 elements 13.1).  Both are even at 64 to 130.
 template <int D>
 cudaError_t append_by_tokens(const AppendParams &p, cudaStream_t st)
 {
