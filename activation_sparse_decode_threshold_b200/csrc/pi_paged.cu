@@ -153,19 +153,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2
     else mma<BF>(d, a, b);
 }
 
-// A number as its 16-bit rounding (low half) and the rounding of what is left (high half).
-template <bool BF>
-__device__ __forceinline__ uint32_t split(float v)
-{
-    if (BF) {
-        const __nv_bfloat16 h = __float2bfloat16(v);
-        const __nv_bfloat162 p = __halves2bfloat162(h, __float2bfloat16(v - __bfloat162float(h)));
-        return *reinterpret_cast<const uint32_t *>(&p);
-    }
-    const __half h = __float2half(v);
-    const __half2 p = __halves2half2(h, __float2half(v - __half2float(h)));
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
 // The two parts' sum.  An infinite high part stands alone: its low part holds 0
 // times that infinity.
 __device__ __forceinline__ float whole(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
@@ -215,6 +202,14 @@ __device__ __forceinline__ uint2 split2(float a, float b)
     const float2 f = __half22float2(h);
     const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
     return make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l));
+}
+
+// Each number as its rounding (low half) and that of what is left (high half).
+template <bool BF>
+__device__ __forceinline__ uint2 parts(float a, float b)
+{
+    const uint2 w = split2<BF>(a, b);
+    return make_uint2(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632));
 }
 
 // Eight consecutive results from shared memory.
@@ -827,6 +822,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         const float f = pow2_of(254 - ref) * 0x1p13f;
         if (FMT == kI4) {
 #pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2 * R; ++e) x[b][e] *= f;
+#pragma unroll
             for (int i = 0; i < P / 2; ++i)
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) {
@@ -846,11 +845,11 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                             a[1][2 * o] = hsub(and_or(z, 0x000f000fu, 0x64006400u), 0x64086408u);
                             a[1][2 * o + 1] = hfma(and_or(z, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
                         }
-                        const float f0 = f * half_of(vs[2 * rt], j), f1 = f * half_of(vs[2 * rt + 1], j);
+                        const float f0 = half_of(vs[2 * rt], j), f1 = half_of(vs[2 * rt + 1], j);
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            const uint2 w = make_uint2(transpose8(split<false>(x[b][2 * rt] * f0)),
-                                                       transpose8(split<false>(x[b][2 * rt + 1] * f1)));
+                            const uint2 v = parts<false>(x[b][2 * rt] * f0, x[b][2 * rt + 1] * f1);
+                            const uint2 w = make_uint2(transpose8(v.x), transpose8(v.y));
                             mma<false>(acc[b][2 * j], a[0], w);
                             mma<false>(acc[b][2 * j + 1], a[1], w);
                         }
@@ -866,7 +865,8 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         x[b][2 * rt] *= __uint_as_float(vs[2 * rt].x) * f;
                         x[b][2 * rt + 1] *= __uint_as_float(vs[2 * rt + 1].x) * f;
                     }
-                    w[b][rt] = make_uint2(transpose8(split<BF>(x[b][2 * rt])), transpose8(split<BF>(x[b][2 * rt + 1])));
+                    const uint2 v = parts<BF>(x[b][2 * rt], x[b][2 * rt + 1]);
+                    w[b][rt] = make_uint2(transpose8(v.x), transpose8(v.y));
                 }
 #pragma unroll
             for (int i = 0; i < KS; ++i)
