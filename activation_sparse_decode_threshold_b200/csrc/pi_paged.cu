@@ -62,7 +62,7 @@ struct Cfg {
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * (kRing + kBuf);
     static_assert(kStages >= 3 && kBuf % 16 == 0 && kRing % 16 == 0 && kSmem + 7168 <= 227 * 1024, "");
-    static_assert(kBuf >= kHeads * kDP * 4 + kHeads * (1 + D / 32) * 4 && 16 * D * NB <= kHeads * kDP * 4, "");
+    static_assert(kBuf >= kHeads * kDP * 4 + kHeads * 4 && 16 * D * NB <= kHeads * kDP * 4, "");
 };
 
 __device__ __forceinline__ uint32_t s2u(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -176,6 +176,17 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
     return r;
 }
 
+// Codes n of 4 bits (at bits 4 i of each half) as fp16 pairs n - 8: under the
+// exponent of 1024 a code is 1024 + n, four bits further up 1024 + 16 n; what
+// leads from there to n - 8 is exact.
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&r)[4])
+{
+    const uint32_t z = w >> 8;
+    r[0] = hsub(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);
+    r[1] = hfma(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+    r[2] = hsub(and_or(z, 0x000f000fu, 0x64006400u), 0x64086408u);
+    r[3] = hfma(and_or(z, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+}
 // Two bytes of w (signed, with the top bit flipped) as an fp16 pair: under the
 // exponent of 1024 a byte b is 1024 + b.
 template <uint32_t SEL>
@@ -489,7 +500,6 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
     };
     // ---- one chunk after the other ---------------------------------------------
     uint2 q[C::kQShared ? 1 : KS][C::kQShared ? 1 : NB];
-    float bias[FMT == kI4 ? D / 32 : 1][NB];   // I4: what the codes' offset of 8 adds to a group's products
     float acc[NB][KS][4] = {};
     float m[NB], l[NB], factor[NB];            // of head 4 b + t; l of positions g and g + 8 only, until the segment's end
 #pragma unroll
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
             // The queries' parts go to the buffer as the products take them: word (i, b, column 4 lanes, t) holds column
             // g's parts of places 2t, 2t + 1 and 2t + 8, 2t + 9 of product i.  Eight lanes share a head here.
             uint32_t *words = reinterpret_cast<uint32_t *>(buf);
-            float *extra = buf + H * DP;   // factors, then biases
+            float *extra = buf + H * DP;   // factors
             const int hl = lane / 8, part = lane % 8;
             if (NB > 1) {   // all on their way to L1 at once
 #pragma unroll
@@ -568,26 +578,23 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     if (!live) v[e] = 0.f;
                     top = fmaxf(top, fabsf(v[e]));
                 }
-                // the head's largest element is brought to [1, 2) (I4: 2^8 times that), so that no part leaves the range
-                // of 16 bits
+                // the head's largest element is brought to [1, 2), so that no part leaves the range of 16 bits
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
                 const int ex = min(max(__float_as_int(top) >> 23, 16), 253);
-                const float down = pow2_of(254 - ex) * (FMT == kI4 ? 0x1p8f : 1.f);
+                const float down = pow2_of(254 - ex);
                 if (part == 0)
-                    extra[4 * b + hl] = pow2_of(ex) * (p.softcap > 0.f ? p.scale * (2.8853900817779268f / p.softcap) : p.scale * 1.4426950408889634f) *
-                                        (FMT == kI4 ? 0x1p16f : 1.f);   // (codes of 4 bits are n 2^-24)
-                float sum = 0.f;
+                    extra[4 * b + hl] = pow2_of(ex) * (p.softcap > 0.f ? p.scale * (2.8853900817779268f / p.softcap) : p.scale * 1.4426950408889634f);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {   // a pair of elements, its product i, its place: word x or y of lanes 4 g + tt
                     const int d = part * E + 2 * e;
                     float x, y;
                     int i, tt, second;
-                    if (FMT == kI4) {   // of 8 elements (0, 4), (1, 5), (2, 6), (3, 7); codes of odd ones are 16 times theirs
+                    if (FMT == kI4) {   // of 8 elements (0, 4), (1, 5), (2, 6), (3, 7)
                         const int at8 = 8 * (e / 4), k = e % 4;
-                        x = v[at8 + k] * (k & 1 ? down * 0x1p-4f : down);
-                        y = v[at8 + k + 4] * (k & 1 ? down * 0x1p-4f : down);
+                        x = v[at8 + k] * down;
+                        y = v[at8 + k + 4] * down;
                         i = d / 32 * 2 + (k >> 1);
                         tt = d / 8 % 4;
                         second = k & 1;
@@ -602,26 +609,12 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     uint32_t *to = words + (((i * NB + b) * 8 + 2 * hl) * 4 + tt) * 2 + second;
                     to[0] = w.x;
                     to[8] = w.y;
-                    if (FMT == kI4) {
-                        const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-                        const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-                        sum += ((hi.x + hi.y) + (lo.x + lo.y)) * (e & 1 ? 16.f : 1.f);
-                    }
-                }
-                if (FMT == kI4) {   // what the codes' offset of 8 adds to a group's products
-                    sum += __shfl_xor_sync(~0u, sum, 1);
-                    if (E == 8) sum += __shfl_xor_sync(~0u, sum, 2);
-                    if (part % (32 / E) == 0) extra[H + part * E / 32 * H + 4 * b + hl] = sum * -0x1p-21f;
                 }
             }
             __syncwarp();
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 factor[b] = extra[4 * b + t];
-                if (FMT == kI4) {
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) bias[FMT == kI4 ? j : 0][b] = extra[H + j * H + 4 * b + t];
-                }
                 m[b] = -FLT_MAX;
                 l[b] = 0.f;
 #pragma unroll
@@ -668,17 +661,15 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int j = 2 * i + h;
-                        const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1], s0 = r0 >> 8, s1 = r1 >> 8;
-                        // a code n at the low end of 16 bits is the number n 2^-24, four bits further up 16 n 2^-24 (the
-                        // queries there are a 16th)
-                        const uint32_t a0[4] = {r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u};
-                        const uint32_t a1[4] = {s0 & 0x000f000fu, s1 & 0x000f000fu, s0 & 0x00f000f0u, s1 & 0x00f000f0u};
+                        uint32_t p0[4], p1[4];   // elements (0, 4), (1, 5), (2, 6), (3, 7) of rows g and g + 8
+                        nibbles(r[2 * h], p0);
+                        nibbles(r[2 * h + 1], p1);
+                        const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
                         const float f0 = half_of(ks[2 * rt], j), f1 = half_of(ks[2 * rt + 1], j);
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            const float off = bias[FMT == kI4 ? j : 0][b];
                             float c[4];
-                            mma<false>(c, a0, query(2 * j, b), off, 0.f, off, 0.f);
+                            mma<false>(c, a0, query(2 * j, b), true);
                             mma<false>(c, a1, query(2 * j + 1, b));
                             x[b][2 * rt] += f0 * (c[0] + c[1]);
                             x[b][2 * rt + 1] += f1 * (c[2] + c[3]);
@@ -834,17 +825,11 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int j = 2 * i + h;
-                        // element 4 g + e of positions 2t, 2t + 1 at bits 4 e: under the exponent of 1024 a code is 1024 + n
-                        // or 1024 + 16 n; less 8 these are exact
-                        uint32_t a[2][4];
-#pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            const uint32_t w = r[2 * h + o], z = w >> 8;
-                            a[0][2 * o] = hsub(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);
-                            a[0][2 * o + 1] = hfma(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
-                            a[1][2 * o] = hsub(and_or(z, 0x000f000fu, 0x64006400u), 0x64086408u);
-                            a[1][2 * o + 1] = hfma(and_or(z, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
-                        }
+                        // element 4 g + e of positions 2t, 2t + 1 at bits 4 e
+                        uint32_t p0[4], p1[4];
+                        nibbles(r[2 * h], p0);
+                        nibbles(r[2 * h + 1], p1);
+                        const uint32_t a[2][4] = {{p0[0], p0[1], p1[0], p1[1]}, {p0[2], p0[3], p1[2], p1[3]}};
                         const float f0 = half_of(vs[2 * rt], j), f1 = half_of(vs[2 * rt + 1], j);
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
