@@ -174,7 +174,7 @@ struct MvCfg {
 // them beside, keeps two or three batches of 4 units under way, and x is brought to
 // each CTA once (for 13 tokens of 8192 columns it is 213 KB, about as much as the
 // CTA's share of the matrix: hence the clusters).  6144x4096, one fp32 token with
-// its norm: 6.9 us (2.05 TB/s); 8192x8192, 13 tokens: 17.5 us (2.2 TB/s).
+// its norm: 6.8 us (2.1 TB/s); 8192x8192, 13 tokens: 17.4 us (2.2 TB/s).
 // PARTS: 3 for F32 x, else 1.  NT: tiles of 8 columns of B (tokens * PARTS).
 template <bool BF, int PARTS, int NT>
 __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p, int log_cs, int clusters, int chunk, int depth, int split)
