@@ -70,18 +70,20 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
     return r;
 }
 
-// Eight nibbles to four 16-bit pairs n - 8.  Under the exponent bits of 1024
-// (fp16) or 128 (bf16) a nibble is that number plus n; in fp16 one four bits
-// further up is 1024 + 16 n, which a product and a sum bring to n - 8 without a
-// shift.  All of it is exact.
+// Eight nibbles to four 16-bit pairs: n - 8 in fp16, (n - 8) / 256 in bf16.  Under
+// the exponent bits of 1024 (fp16) a nibble is that number plus n, and one four
+// bits further up 1024 + 16 n, which a product and a sum bring to n - 8 without a
+// shift; under those of 1/2 (bf16) it is 1/2 + n / 256.  All of it is exact.  The
+// 256 keeps a group's 32 products of x up to bf16's or fp32's largest number in
+// range, since their sum is at most max |x|; y gets it back at the end (kUnit).
 template <bool BF>
 __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&r)[4])
 {
     if (BF) {
-        const uint32_t bias = 0x43084308u;   // 136
+        const uint32_t bias = 0x3f083f08u;   // 136 / 256
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t v = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
+            const uint32_t v = and_or(w >> (4 * i), 0x000f000fu, 0x3f003f00u);
             const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&bias));
             r[i] = *reinterpret_cast<const uint32_t *>(&d);
         }
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
 {
     using C = MvCfg<NT>;
     constexpr int W = C::kWarps, T = C::kThreads, U = C::kBatch;
+    constexpr float kUnit = BF ? 256.f : 1.f;   // of the sums (nibbles())
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float ssq[kInt4MaxTokens * W];
     __shared__ float total_sq[kInt4MaxTokens];
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                     if (p.eps > 0.f) ss += peer(total_sq + t, c);
                 }
             }
-            if (p.eps > 0.f) y *= 1.f / sqrtf(ss / float(p.k) + p.eps);
+            y *= p.eps > 0.f ? kUnit / sqrtf(ss / float(p.k) + p.eps) : kUnit;
             if (p.add) y += add;
             if (at >= 0) {
                 if (p.yt == kF32) reinterpret_cast<float *>(p.y)[at] = y;
