@@ -150,6 +150,21 @@ __device__ __forceinline__ float value_of(const uint8_t *p, long long i, int dt)
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
+// unit / sqrt(mean x^2 + eps) for a token whose squares' sum leaves fp32 (numbers
+// beyond some 1e18): summed again in 64 bits, by the half warp that needs it.
+__device__ __noinline__ float root_inv_in_64(const uint8_t *x, long long at, int dt, int k, float eps, float unit)
+{
+    double ss = 0;
+#pragma unroll 1
+    for (int c = threadIdx.x % 16; c < k; c += 16) {
+        const double v = value_of(x, at + c, dt);
+        ss = fma(v, v, ss);
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), ss, o);
+    return float(unit * rsqrt(ss / k + eps));
+}
+
 // A product's shape in shared memory.  W: warps of a CTA.
 template <int NT>
 struct MvCfg {
@@ -176,9 +191,11 @@ struct MvCfg {
 // them beside, keeps two or three batches of 4 units under way, and x is brought to
 // each CTA once (for 13 tokens of 8192 columns it is 213 KB, about as much as the
 // CTA's share of the matrix: hence the clusters).  6144x4096, one fp32 token with
-// its norm: 6.8 us (2.1 TB/s); 8192x8192, 13 tokens: 17.4 us (2.2 TB/s).
-// PARTS: 3 for F32 x, else 1.  NT: tiles of 8 columns of B (tokens * PARTS).
-template <bool BF, int PARTS, int NT>
+// its norm: 6.8 us (2.1 TB/s); 8192x8192, 13 tokens: 17.0 us (2.3 TB/s).
+// PARTS: 3 for F32 x, else 1.  NT: tiles of 8 columns of B (tokens * PARTS).  NORM:
+// eps > 0; a kernel of its own, since what the norm needs costs the others registers
+// (8192x8192, 13 tokens without a norm, by one kernel for both: 17.6 us).
+template <bool BF, int PARTS, int NT, bool NORM>
 __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p, int log_cs, int clusters, int chunk, int depth, int split)
 {
     using C = MvCfg<NT>;
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                     const int t = i / split, part_of = i - t * split;
                     uint16_t *row = xs + t * stride;
                     float ss = 0.f;
-                    const bool squares = p.eps > 0.f && t0 == t_begin;
+                    const bool squares = NORM && t0 == t_begin;
 #pragma unroll 4
                     for (int c = part_of * 32 + lane; c < pieces; c += 32 * split) {
                         const int col = k0 * 64 + 8 * c;
@@ -298,7 +315,7 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
                     }
                 }
                 __syncthreads();
-                if (p.eps > 0.f && t0 == t_begin && threadIdx.x < p.tokens) {
+                if (NORM && t0 == t_begin && threadIdx.x < p.tokens) {
                     float ss = k0 == k_begin ? 0.f : total_sq[threadIdx.x];
                     for (int i = 0; i < split; ++i) ss += ssq[threadIdx.x * split + i];
                     total_sq[threadIdx.x] = ss;
@@ -401,14 +418,18 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
             float y = 0.f, ss = 0.f;
             if (cs == 1) {
                 y = sums[sum];
-                if (p.eps > 0.f) ss = total_sq[t];
+                if (NORM) ss = total_sq[t];
             } else {
                 for (int c = 0; c < cs; ++c) {
                     y += peer(sums + sum, c);
-                    if (p.eps > 0.f) ss += peer(total_sq + t, c);
+                    if (NORM) ss += peer(total_sq + t, c);
                 }
             }
-            y *= p.eps > 0.f ? kUnit / sqrtf(ss / float(p.k) + p.eps) : kUnit;
+            float factor = kUnit;
+            if (NORM) factor = kUnit / sqrtf(ss / float(p.k) + p.eps);
+            // (a mean above 2^104, infinity included; fp16 numbers stay below, a NaN is one)
+            if (BF && NORM && factor < 0x1p-44f) factor = root_inv_in_64(p.x, t * p.xs, p.xt, p.k, p.eps, kUnit);
+            y *= factor;
             if (p.add) y += add;
             if (at >= 0) {
                 if (p.yt == kF32) reinterpret_cast<float *>(p.y)[at] = y;
@@ -422,12 +443,12 @@ __global__ void __launch_bounds__(MvCfg<NT>::kThreads, 1) k_matvec(Int4Params p,
     }
 }
 
-template <bool BF, int PARTS, int NT>
+template <bool BF, int PARTS, int NT, bool NORM>
 cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
 {
     using C = MvCfg<NT>;
     static_assert((C::kRoom - C::fixed(C::kLeastDepth, kInt4MaxTokens)) / (8 * NT) >= 64 + 4 * 128, "a chunk of x has 4 units at least");
-    if (set) return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRoom);
+    if (set) return cudaFuncSetAttribute(k_matvec<BF, PARTS, NT, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRoom);
     const int cols = p.tokens * PARTS, tiles = (p.n + 15) / 16;
     // Over how many CTAs the columns are split: so many that x's part fits into shared memory at once (13 tokens of 8192
     // columns: two), beside rings as deep as then there is room for; for a CTA of its own three batches deep (8 tokens
@@ -441,34 +462,40 @@ cudaError_t launch(const Int4Params &p, cudaStream_t st, bool set)
     if (chunk > units) chunk = units;
     int clusters = cs == 1 ? p.n_sm : p.clusters[cs == 2 ? 0 : cs == 4 ? 1 : 2];
     if (clusters > tiles) clusters = tiles;
-    return launch_close(k_matvec<BF, PARTS, NT>, dim3(clusters * cs), C::kThreads, C::fixed(depth, p.tokens) + cols * (chunk * 64 + 32) * 2,
+    return launch_close(k_matvec<BF, PARTS, NT, NORM>, dim3(clusters * cs), C::kThreads, C::fixed(depth, p.tokens) + cols * (chunk * 64 + 32) * 2,
                         st, cs, p, cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3, clusters, chunk, depth,
                         p.tokens < C::kWarps ? C::kWarps / p.tokens : 1);
 }
 
-template <bool BF, int PARTS>
+template <bool BF, int PARTS, bool NORM>
 cudaError_t by_columns(int nt, const Int4Params &p, cudaStream_t st, bool set)
 {
     switch (nt) {
-    case 1: return launch<BF, PARTS, 1>(p, st, set);
-    case 2: return launch<BF, PARTS, 2>(p, st, set);
-    case 3: return launch<BF, PARTS, 3>(p, st, set);
-    case 4: return launch<BF, PARTS, 4>(p, st, set);
-    case 6: return launch<BF, PARTS, PARTS == 3 ? 6 : 1>(p, st, set);
-    case 9: return launch<BF, PARTS, PARTS == 3 ? 9 : 1>(p, st, set);
-    default: return launch<BF, PARTS, PARTS == 3 ? 12 : 1>(p, st, set);
+    case 1: return launch<BF, PARTS, 1, NORM>(p, st, set);
+    case 2: return launch<BF, PARTS, 2, NORM>(p, st, set);
+    case 3: return launch<BF, PARTS, 3, NORM>(p, st, set);
+    case 4: return launch<BF, PARTS, 4, NORM>(p, st, set);
+    case 6: return launch<BF, PARTS, PARTS == 3 ? 6 : 1, NORM>(p, st, set);
+    case 9: return launch<BF, PARTS, PARTS == 3 ? 9 : 1, NORM>(p, st, set);
+    default: return launch<BF, PARTS, PARTS == 3 ? 12 : 1, NORM>(p, st, set);
     }
 }
 
-cudaError_t dispatch(const Int4Params &p, cudaStream_t st, bool set)
+template <bool NORM>
+cudaError_t by_type(const Int4Params &p, cudaStream_t st, bool set)
 {
     if (p.xt == kF32) {
         const int cols = 3 * p.tokens;
         const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 24 ? 3 : cols <= 32 ? 4 : cols <= 48 ? 6 : cols <= 72 ? 9 : 12;
-        return by_columns<true, 3>(nt, p, st, set);
+        return by_columns<true, 3, NORM>(nt, p, st, set);
     }
     const int nt = (p.tokens + 7) / 8;
-    return p.xt == kF16 ? by_columns<false, 1>(nt, p, st, set) : by_columns<true, 1>(nt, p, st, set);
+    return p.xt == kF16 ? by_columns<false, 1, NORM>(nt, p, st, set) : by_columns<true, 1, NORM>(nt, p, st, set);
+}
+
+cudaError_t dispatch(const Int4Params &p, cudaStream_t st, bool set)
+{
+    return p.eps > 0.f ? by_type<true>(p, st, set) : by_type<false>(p, st, set);
 }
 
 }  // namespace
@@ -477,11 +504,14 @@ cudaError_t int4_setup()
 {
     Int4Params p{};
     for (int xt : {int(kF32), int(kF16), int(kBF16)})
-        for (p.tokens = 1; p.tokens <= kInt4MaxTokens; ++p.tokens) {
-            p.xt = xt;
-            const cudaError_t e = dispatch(p, nullptr, true);
-            if (e != cudaSuccess) return e;
-        }
+        for (int tokens : {1, 3, 6, 9, 11, 17, 25})   // of each number of tiles
+            for (float eps : {0.f, 1.f}) {
+                p.xt = xt;
+                p.tokens = tokens;
+                p.eps = eps;
+                const cudaError_t e = dispatch(p, nullptr, true);
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 
@@ -498,7 +528,7 @@ cudaError_t int4_clusters(int (&clusters)[3])
         cfg.dynamicSmemBytes = MvCfg<4>::kRoom;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], k_matvec<true, 3, 4>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], k_matvec<true, 3, 4, true>, &cfg);
         if (e != cudaSuccess) return e;
         if (clusters[i] < 1) clusters[i] = 1;
     }

@@ -389,7 +389,8 @@ PI_API void pi_int4_destroy(pi_int4_t m);
  *   y_dev    n_tokens rows of n_rows values [y_dtype], y_stride elements apart
  * Types F32, F16 or BF16.  Products are exact (x in parts that hold all its
  * bits), sums are fp32 (of 1/256 of the terms for F32 and BF16 x, so that x up to
- * its type's largest number is fine while the sums of s x stay below that), y is
+ * its type's largest number is fine while the sums of s x stay below that; the
+ * norm's factor comes last, and its squares may leave fp32's range), y is
  * rounded once.  Each token's row comes from that
  * token alone (the order of its sums, and so its last bits, may differ with
  * n_tokens), the result is deterministic, and calls on several streams may

@@ -29,3 +29,25 @@ def test_matvec_largest_numbers(made, dt, n, k, tokens):
     want, bound = R.matvec(q, s, x, torch.float32)
     assert want.abs().max() < 0.9 * top
     check(y, want, bound)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,k,tokens", [(40, 96, 1), (33, 416, 7), (70, 8192, 13), (24, 8192, 32)])
+def test_matvec_norm_of_large_and_small_numbers(made, dt, n, k, tokens):
+    """Tokens whose squares leave fp32's range (above 1.8e19), beside ordinary ones, zeros and small ones."""
+    g = gen(n + tokens)
+    q, s = R.encode_int4(torch.randn(n, k, generator=g) * 0.05)
+    sizes = torch.tensor([1e20, 1.0, 1e30, 0.0, 1e36, 1e19, 1e-20])[torch.arange(tokens) % 7]
+    x = (torch.randn(tokens, k, generator=g) * sizes[:, None]).to(R.DT[dt])
+    if tokens > 1:
+        x[1, 5] = 1e22                                                 # one large element among ordinary ones
+    y = torch.zeros(tokens, n, device="cuda")
+    B.pi_int4_matvec(matrix(made, q, s), x.cuda(), y, norm_eps=1e-6)
+    want, bound = R.matvec(q, s, x, torch.float32, eps=1e-6)
+    check(y, want, bound)
+    # without a norm the same numbers stay apart too: nothing of one token gets into another
+    alone = torch.zeros(1, n, device="cuda")
+    for t in (0, tokens - 1):
+        B.pi_int4_matvec(matrix(made, q, s), x[t:t + 1].cuda(), alone, norm_eps=1e-6)
+        want, bound = R.matvec(q, s, x[t:t + 1], torch.float32, eps=1e-6)
+        check(alone, want, bound)
