@@ -206,7 +206,20 @@ __device__ __forceinline__ void norm_rotate(const AppendParams &p, const float (
         for (int e = 0; e < N; ++e) ss += x[e] * x[e];
 #pragma unroll
         for (int o = D / N / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        const T r = root_inv(ss * T(1.0 / D) + T(p.eps));
+        T r = root_inv(ss * T(1.0 / D) + T(p.eps));
+        // fp32 squares end at numbers of some 1e19: the heads that have larger ones are normed at 2^-80 of their size
+        if (sizeof(T) == 4 && __any_sync(~0u, !(ss < T(0x1p120f)))) {
+            const T down = ss < T(0x1p120f) ? T(1) : T(0x1p-80f);
+            ss = 0;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                x[e] *= down;
+                ss += x[e] * x[e];
+            }
+#pragma unroll
+            for (int o = D / N / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+            r = root_inv(ss * T(1.0 / D) + T(p.eps) * down * down);
+        }
 #pragma unroll
         for (int e = 0; e < N; ++e) x[e] = x[e] * r * T(w[e]);
     }

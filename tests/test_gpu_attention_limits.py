@@ -51,3 +51,30 @@ def test_matvec_norm_of_large_and_small_numbers(made, dt, n, k, tokens):
         B.pi_int4_matvec(matrix(made, q, s), x[t:t + 1].cuda(), alone, norm_eps=1e-6)
         want, bound = R.matvec(q, s, x[t:t + 1], torch.float32, eps=1e-6)
         check(alone, want, bound)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tokens", [3, 200])     # (4 and 8 elements to a lane)
+def test_append_norm_of_large_queries(made, dt, dim, tokens):
+    """Heads whose squares leave fp32's range are normed like all others, queries and keys."""
+    g = gen(dim + tokens)
+    heads, kv, eps = 6, 2, 1e-6
+    c = R.Cache(g, [tokens], kv, dim, "bf16", 16, fill=False).cuda()
+    a = layer(made, heads, kv, dim, cache_dtype="bf16", page_size=16, rotary_dim=dim, norm_eps=eps)
+    sizes = torch.tensor([1e20, 1.0, 1e-3, 1e37, 1e19])
+    mk = lambda h: torch.randn(tokens, h, dim, generator=g) * sizes[torch.arange(tokens * h) % 5].view(tokens, h, 1)  # noqa: E731
+    q, k, v = mk(heads).to(R.DT[dt]), mk(kv).to(R.DT[dt]), torch.randn(tokens, kv, dim, generator=g).to(R.DT[dt])
+    q[0, 0, 0] = torch.finfo(R.DT[dt]).max
+    w = 1 + 0.3 * torch.randn(dim, generator=g)
+    out = torch.zeros(tokens, heads, dim, dtype=R.DT[dt], device="cuda")
+    pos, seq = torch.arange(tokens, dtype=torch.int32).cuda(), torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    B.pi_kv_append(a, cache_of(c), c.table_dev, pos, q.cuda(), k.cuda(), v.cuda(), out, seq=seq, q_norm=w.cuda(), k_norm=w.cuda())
+    assert B.pi_attn_sync(a) == B.PI_OK
+    rows = c.rows("k", 0, 0, tokens)
+    for t in range(tokens):
+        x, mag = R.norm_rotate(q[t], t, dim, False, 10000.0, eps, w)
+        # (as in test_gpu_attention.py: the norm's sum, root and products, the rotation)
+        check(out[t], x, mag * (dim / 32 + 5 + 8 + 6) * R.U + R.half_step(x, R.DT[dt]), f"q {t}")
+        x, _ = R.norm_rotate(k[t], t, dim, False, 10000.0, eps, w)
+        check(rows[t], x, R.half_step(x, torch.bfloat16) + x.abs() * R.U, f"k {t}")
