@@ -13,8 +13,11 @@
 // for the scores, elements of V for the sums) and 4 query heads as 8 columns:
 // column 2h holds head h's queries or weights in 16 bits, column 2h + 1 what
 // that rounding left, so that the products are those of 22 (bf16: 16) bits with
-// the cache's 16-, 8- or 4-bit numbers, which are exact.  A head's two columns
-// meet in one lane.  Scales of quantised rows are applied in fp32, to the scores
+// the cache's 16-, 8- or 4-bit numbers, which are exact.  Over a bf16 cache 16 bits
+// are all that F16 and BF16 callers' queries and results have; F32 callers get 24
+// (WIDE): each product twice, with half the rounding in both first columns, and
+// what is left in two parts (32 texts of 4096 positions, 4 queries to a cached head:
+// 106.1 us instead of 103.5; 16 texts, 16 queries to a head of 64: 57.5, 50.0).  A head's two columns meet in one lane.  Scales of quantised rows are applied in fp32, to the scores
 // (K) and to the weights (V).
 //
 // Measured: 32 ragged texts of bf16 (525 MB) 103 us, 5.1 TB/s; 32768 positions of
@@ -38,8 +41,10 @@ constexpr int kStart = 2;
 constexpr int kSlots = 32;            // partial results of a CTA's warps, at most (2 for each)
 
 // FMT: the cache's format.  NB: tiles of 4 query heads that share a cached head.
-template <int FMT, int D, int NB>
+// WIDE: F32 queries and results over a bf16 cache.
+template <int FMT, int D, int NB, bool WIDE = false>
 struct Cfg {
+    static_assert(!WIDE || FMT == kBF16, "");
     static constexpr bool kF = FMT == kF16 || FMT == kBF16;
     static constexpr int kRow = FMT == kI8 ? D : FMT == kI4 ? D / 2 : 2 * D;   // bytes of a cached row
     static constexpr int kScale = FMT == kI8 ? 4 : FMT == kI4 ? D / 16 : 0;    // bytes of its scales
@@ -51,18 +56,19 @@ struct Cfg {
     static constexpr int kStage = kOffI + 16;
     static constexpr int kHeads = 4 * NB;                                     // query heads of an item
     static constexpr int kStep = D / 16;                                      // products of 16 along the head
-    static constexpr bool kQShared = NB * D >= 512;                           // queries stay in shared memory
+    static constexpr bool kQShared = WIDE || NB * D >= 512;                   // queries stay in shared memory
     static constexpr int kDP = D + 8;                                         // a head's distance in a partial result
     static constexpr int kPart = kHeads * (kDP + 2) * 4;                      // its bytes: o, then m and l
-    static constexpr int kBuf = kHeads * (kDP + 8) * 4;                       // a warp's: queries, later its result
+    static constexpr int kOffQ2 = kHeads * (kDP + 8) * 4;                     // WIDE: the queries' last parts
+    static constexpr int kBuf = kOffQ2 + (WIDE ? 8 * D * NB : 0);             // a warp's: queries, later its result
     // Warps of a CTA: as many as registers and three stages each allow.
-    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : NB == 2 ? 6 : 8) : NB * D == 64 && FMT != kI8 ? 16 : NB * D <= 128 ? 12 : 8;
+    static constexpr int kWarps = kF && D == 128 ? (NB == 4 ? 4 : NB == 2 ? 6 : 8) : NB * D == 64 && FMT != kI8 && !WIDE ? 16 : NB * D <= 128 ? 12 : 8;
     static constexpr int kRoom = 220 * 1024 / kWarps / 16 * 16;
     static constexpr int kStages = (kRoom - kBuf) / kStage < 8 ? (kRoom - kBuf) / kStage : 8;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * (kRing + kBuf);
     static_assert(kStages >= 3 && kBuf % 16 == 0 && kRing % 16 == 0 && kSmem + 7168 <= 227 * 1024, "");
-    static_assert(kBuf >= kHeads * kDP * 4 + kHeads * 4 && 16 * D * NB <= kHeads * kDP * 4, "");
+    static_assert(kOffQ2 >= kHeads * kDP * 4 + kHeads * 4 && 16 * D * NB <= kHeads * kDP * 4, "");
 };
 
 __device__ __forceinline__ uint32_t s2u(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -215,14 +221,27 @@ __device__ __forceinline__ uint2 split2(float a, float b)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&l));
 }
 
+// Two numbers' words (rounding; what is left) as one word for each: its pair of columns.
+__device__ __forceinline__ uint2 columns(uint2 w) { return make_uint2(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632)); }
 // Each number as its rounding (low half) and that of what is left (high half).
 template <bool BF>
 __device__ __forceinline__ uint2 parts(float a, float b)
 {
-    const uint2 w = split2<BF>(a, b);
-    return make_uint2(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632));
+    return columns(split2<BF>(a, b));
 }
 
+// Two numbers in 24 bits, for two products: half their rounding (twice, so that an
+// infinity of the cache meets no zero there) with what is left, and with what that left.
+__device__ __forceinline__ void split4(float a, float b, uint2 &first, uint2 &second)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 half = __floats2bfloat162_rn(0.5f * f.x, 0.5f * f.y);
+    const uint2 rest = split2<true>(a - f.x, b - f.y);
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(&half);
+    first = make_uint2(u, rest.x);
+    second = make_uint2(u, rest.y);
+}
 // Eight consecutive results from shared memory.
 __device__ __forceinline__ void output8(uint8_t *p, long long i, int dt, const float *v)
 {
@@ -304,10 +323,10 @@ constexpr int kLeastRef = 16;
 // A power of two from its exponent.
 __device__ __forceinline__ float pow2_of(int biased) { return __int_as_float(biased << 23); }
 
-template <int FMT, int D, int NB>
-__global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnParams p, int items, int blocks_per_head)
+template <int FMT, int D, int NB, bool WIDE>
+__global__ void __launch_bounds__(32 * Cfg<FMT, D, NB, WIDE>::kWarps, 1) k_paged(AttnParams p, int items, int blocks_per_head)
 {
-    using C = Cfg<FMT, D, NB>;
+    using C = Cfg<FMT, D, NB, WIDE>;
     constexpr bool BF = FMT == kBF16;
     constexpr int W = C::kWarps, S = C::kStages, T = 32 * W, KS = C::kStep, P = C::kPieces, DP = C::kDP, H = C::kHeads;
     constexpr int R = C::kTiles, CH = C::kChunk;
@@ -605,8 +624,14 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         tt = FMT == kI8 ? d / 4 % 4 : d / 2 % 4;
                         second = FMT == kI8 ? d / 2 % 2 : d / 8 % 2;
                     }
-                    const uint2 w = split2<BF>(x, y);
                     uint32_t *to = words + (((i * NB + b) * 8 + 2 * hl) * 4 + tt) * 2 + second;
+                    uint2 w, w2;
+                    if (WIDE) {
+                        split4(x, y, w, w2);
+                        words[C::kOffQ2 / 4 + (((i * NB + b) * 4 + hl) * 4 + tt) * 2 + second] = w2.y;
+                    } else {
+                        w = split2<BF>(x, y);
+                    }
                     to[0] = w.x;
                     to[8] = w.y;
                 }
@@ -630,7 +655,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
         auto query = [&](int i, int b) {
             return C::kQShared ? reinterpret_cast<const uint2 *>(buf)[(i * NB + b) * 32 + lane] : q[C::kQShared ? 0 : i][C::kQShared ? 0 : b];
         };
-
+        // (of the second products: the first columns are the first product's)
+        auto query2 = [&](int i, int b) {
+            return g & 1 ? reinterpret_cast<const uint2 *>(buf + C::kOffQ2 / 4)[(i * NB + b) * 16 + g / 2 * 4 + t] : query(i, b);
+        };
 
         // ---- scores of head 4 b + t at positions 16 r + g and 16 r + g + 8
         float x[NB][2 * R];
@@ -700,7 +728,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         uint32_t r[4];
                         ldm4<false>(base + 16 * place(mat_row + 16 * rt, 2 * i + mat_piece), r);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) mma<BF>(c[b][rt][i % CC], r, query(i, b), i < CC);
+                        for (int b = 0; b < NB; ++b) {
+                            mma<BF>(c[b][rt][i % CC], r, query(i, b), i < CC);
+                            if (WIDE) mma<BF>(c[b][rt][i % CC], r, query2(i, b));
+                        }
                     }
                 }
 #pragma unroll
@@ -841,7 +872,7 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     }
                 }
         } else {
-            uint2 w[NB][R];
+            uint2 w[NB][R], w2[WIDE ? NB : 1][R];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -850,7 +881,16 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                         x[b][2 * rt] *= __uint_as_float(vs[2 * rt].x) * f;
                         x[b][2 * rt + 1] *= __uint_as_float(vs[2 * rt + 1].x) * f;
                     }
-                    const uint2 v = parts<BF>(x[b][2 * rt], x[b][2 * rt + 1]);
+                    uint2 v;
+                    if (WIDE) {
+                        uint2 v2;
+                        split4(x[b][2 * rt], x[b][2 * rt + 1], v, v2);
+                        v = columns(v);
+                        v2 = columns(v2);
+                        w2[WIDE ? b : 0][rt] = make_uint2(transpose8(v2.x), transpose8(v2.y));
+                    } else {
+                        v = parts<BF>(x[b][2 * rt], x[b][2 * rt + 1]);
+                    }
                     w[b][rt] = make_uint2(transpose8(v.x), transpose8(v.y));
                 }
 #pragma unroll
@@ -874,7 +914,10 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
                     } else {
                         ldm4<true>(base + C::kOffV + 16 * place(mat_row_v + 16 * rt, 2 * i + mat_piece_v), r);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) mma<BF>(acc[b][i], r, w[b][rt]);
+                        for (int b = 0; b < NB; ++b) {
+                            mma<BF>(acc[b][i], r, w[b][rt]);
+                            if (WIDE) mma<BF>(acc[b][i], r, w2[WIDE ? b : 0][rt]);
+                        }
                     }
                 }
         }
@@ -1118,29 +1161,35 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB>::kWarps, 1) k_paged(AttnP
 // Query heads that share a cached head are taken 4, 8 or 16 at a time.
 int tiles_of(int group) { return group <= 4 ? 1 : group <= 8 ? 2 : 4; }
 
-template <int FMT, int D, int NB>
+template <int FMT, int D, int NB, bool WIDE>
 cudaError_t launch(const AttnParams &p, cudaStream_t st, bool set)
 {
-    using C = Cfg<FMT, D, NB>;
-    if (set) return cudaFuncSetAttribute(k_paged<FMT, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    using C = Cfg<FMT, D, NB, WIDE>;
+    if (set) return cudaFuncSetAttribute(k_paged<FMT, D, NB, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     const int blocks = (p.group + C::kHeads - 1) / C::kHeads;
-    return launch_close(k_paged<FMT, D, NB>, dim3(p.n_sm), 32 * C::kWarps, C::kSmem, st, 1, p, p.kv_heads * blocks, blocks);
+    return launch_close(k_paged<FMT, D, NB, WIDE>, dim3(p.n_sm), 32 * C::kWarps, C::kSmem, st, 1, p, p.kv_heads * blocks, blocks);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool WIDE>
 cudaError_t by_group(const AttnParams &p, cudaStream_t st, bool set)
 {
     switch (tiles_of(p.group)) {
-    case 1: return launch<FMT, D, 1>(p, st, set);
-    case 2: return launch<FMT, D, 2>(p, st, set);
-    default: return launch<FMT, D, 4>(p, st, set);
+    case 1: return launch<FMT, D, 1, WIDE>(p, st, set);
+    case 2: return launch<FMT, D, 2, WIDE>(p, st, set);
+    default: return launch<FMT, D, 4, WIDE>(p, st, set);
     }
+}
+
+template <int FMT, int D>
+cudaError_t by_bits(const AttnParams &p, cudaStream_t st, bool set)
+{
+    return FMT == kBF16 && p.dt == kF32 ? by_group<FMT, D, FMT == kBF16>(p, st, set) : by_group<FMT, D, false>(p, st, set);
 }
 
 template <int FMT>
 cudaError_t by_dim(const AttnParams &p, cudaStream_t st, bool set)
 {
-    return p.dim == 128 ? by_group<FMT, 128>(p, st, set) : by_group<FMT, 64>(p, st, set);
+    return p.dim == 128 ? by_bits<FMT, 128>(p, st, set) : by_bits<FMT, 64>(p, st, set);
 }
 
 cudaError_t dispatch(const AttnParams &p, cudaStream_t st, bool set)
@@ -1170,13 +1219,15 @@ cudaError_t attn_setup()
     AttnParams p{};
     for (int fmt : {int(kF16), int(kBF16), int(kI8), int(kI4)})
         for (int dim : {64, 128})
-            for (int group : {4, 8, 16}) {
-                p.c.fmt = fmt;
-                p.dim = dim;
-                p.group = group;
-                const cudaError_t e = dispatch(p, nullptr, true);
-                if (e != cudaSuccess) return e;
-            }
+            for (int group : {4, 8, 16})
+                for (int dt : {int(kF16), int(kF32)}) {
+                    p.c.fmt = fmt;
+                    p.dim = dim;
+                    p.group = group;
+                    p.dt = dt;
+                    const cudaError_t e = dispatch(p, nullptr, true);
+                    if (e != cudaSuccess) return e;
+                }
     return cudaSuccess;
 }
 

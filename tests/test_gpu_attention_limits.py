@@ -78,3 +78,48 @@ def test_append_norm_of_large_queries(made, dt, dim, tokens):
         check(out[t], x, mag * (dim / 32 + 5 + 8 + 6) * R.U + R.half_step(x, R.DT[dt]), f"q {t}")
         x, _ = R.norm_rotate(k[t], t, dim, False, 10000.0, eps, w)
         check(rows[t], x, R.half_step(x, torch.bfloat16) + x.abs() * R.U, f"k {t}")
+
+
+def one_hot(cache, lens, kv_heads, dim, page, k_at, k_value, v_at, v_value):
+    """A cache whose keys and values have one element each that is not zero: (position, head) -> element."""
+    c = R.Cache(gen(0), lens, kv_heads, dim, cache, page, fill=False)
+    ks, vs = (torch.zeros(c.pages, kv_heads, page, dim) for _ in range(2))
+    for s, n in enumerate(lens):
+        for p in range(n):
+            at = int(c.table[s, p // page]), slice(None), p % page
+            ks[at][:, k_at(p)] = k_value
+            vs[at][:, v_at(p)] = v_value(p)
+    c.k, c.k_scale = R.encode(ks, cache)
+    c.v, c.v_scale = R.encode(vs, cache)
+    return c.cuda()
+
+
+@pytest.mark.parametrize("dim,kv_heads,group", [(64, 2, 1), (128, 1, 4), (64, 1, 8), (128, 2, 7), (64, 2, 16), (128, 1, 24)])
+def test_scores_of_fp32_queries_over_bf16_keep_their_bits(made, dim, kv_heads, group):
+    """One position with one product: the log of the sum is the score itself, q scale.  fp32 roundings on the way: scale
+    log2 e (its constant and a product), the score's product, the log's two, and one to spare."""
+    lens = [1] * 5
+    c = one_hot("bf16", lens, kv_heads, dim, 16, lambda p: 7, 1.0, lambda p: 3, lambda p: 1.0)
+    q = torch.randn(5, kv_heads * group, dim, generator=gen(dim + group)) * 8
+    a, q, out, lse = attend(made, c, lens, kv_heads * group, "f32", q=q)
+    want = q[:, :, 7].double() / math.sqrt(dim)
+    check(lse, want, want.abs() * 6 * R.U + 2.0 ** -149)
+    assert torch.equal(out[:, :, 3].cpu(), torch.ones(5, kv_heads * group))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,kv_heads,group", [(64, 2, 1), (128, 1, 4), (64, 1, 8), (128, 2, 7), (64, 2, 16), (128, 1, 24)])
+def test_weights_of_fp32_callers_keep_their_bits(made, cache, dim, kv_heads, group):
+    """Two positions of scores 0 and s in (-1, 0), values 0 and 1: out = w / (1 + w), w = e^s, the same w above and below.
+    Roundings relative to out: the score 6 steps of s (test above), exp2 2^-22, the fp16 weight's two parts or the bf16
+    one's three 2^-23 (x - m + 14 for fp16: half a step of 16, 2^-20 log 2 / 2), sums, quotient and products 12 steps."""
+    n = 60
+    lens = [2] * n
+    c = one_hot(cache, lens, kv_heads, dim, 16, lambda p: p, 1.0, lambda p: 0, lambda p: float(p))
+    q = torch.zeros(n, kv_heads * group, dim)
+    q[:, :, 1] = -torch.rand(n, kv_heads * group, generator=gen(group)) * math.sqrt(dim)
+    a, q, out, lse = attend(made, c, lens, kv_heads * group, "f32", q=q)
+    s = q[:, :, 1].double() / math.sqrt(dim)
+    want = torch.sigmoid(s)
+    rel = 6 * R.U + 2.0 ** -22 + 2.0 ** -23 + 12 * R.U + (2.0 ** -21 * math.log(2) if cache == "f16" else 0)
+    check(out[:, :, 0], want, want * rel)
