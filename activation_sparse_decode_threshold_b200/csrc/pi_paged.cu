@@ -17,8 +17,9 @@
 // are all that F16 and BF16 callers' queries and results have; F32 callers get 24
 // (WIDE): each product twice, with half the rounding in both first columns, and
 // what is left in two parts (32 texts of 4096 positions, 4 queries to a cached head:
-// 106.1 us instead of 103.5; 16 texts, 16 queries to a head of 64: 57.5, 50.0).  A head's two columns meet in one lane.  Scales of quantised rows are applied in fp32, to the scores
-// (K) and to the weights (V).
+// 106.1 us instead of 103.5; 16 texts, 16 queries to a head of 64: 57.5, 50.0).  A
+// head's two columns meet in one lane.  Scales of quantised rows are applied in
+// fp32, to the scores (K) and to the weights (V).
 //
 // Measured: 32 ragged texts of bf16 (525 MB) 103 us, 5.1 TB/s; 32768 positions of
 // 4 bits 23.9 us, of which 12 are its chunks' instructions and 10 the way to the
@@ -124,7 +125,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
 
 constexpr float kLargeCap = 64.f;
 // cap * tanh(y / cap) for x = 2 log2 e * y / cap.
-__device__ __noinline__ float large_cap(float x, float cap) { return cap * tanhf(0.34657359f * x); }
+__device__ __noinline__ float whole_cap(float x, float cap) { return cap * tanhf(0.34657359f * x); }
 
 // 1 / x within 2^-23 of it.
 __device__ __forceinline__ float reciprocal(float x)
@@ -751,18 +752,19 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB, WIDE>::kWarps, 1) k_paged
                 }
         }
         // what the mask leaves out is -infinity; cap * tanh(y / cap) = cap - 2 cap / (1 + e^(2y / cap)), which is off by
-        // cap 2^-21 at most: for large caps, whose scores are small beside them, tanh itself
+        // cap 2^-21 at most: for large caps, whose scores are small beside them, and for F32 callers tanh itself
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 2 * R; ++e) x[b][e] *= factor[b];
         if (p.softcap > 0.f) {
             const float cap = p.softcap * 1.4426950408889634f;
+            const bool itself = p.softcap > kLargeCap || p.dt == kF32;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int e = 0; e < 2 * R; ++e)
-                    x[b][e] = p.softcap > kLargeCap ? large_cap(x[b][e], cap) : fmaf(-2.f * cap, reciprocal(1.f + exp2_(x[b][e])), cap);
+                    x[b][e] = itself ? whole_cap(x[b][e], cap) : fmaf(-2.f * cap, reciprocal(1.f + exp2_(x[b][e])), cap);
         }
         if (mask != (CH == 32 ? ~0u : 0xffffu)) {
 #pragma unroll

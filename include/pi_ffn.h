@@ -497,9 +497,11 @@ PI_API pi_status pi_kv_read(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_t
  * A sequence of length 0 gives out = 0 and lse = -infinity.  A negative length
  * counts as 0, one above width * page_size as that (both are reported).
  * Rows of the cache outside the window are not read.  Scores, maxima and sums are
- * fp32.  Queries and weights enter the products in 22 bits or more; over a BF16
- * cache in 24 for dtype F32 and 16 for F16 and BF16 (which hold such a query
- * whole).  Over I8 and INT4G32 caches a weight times its V scale is held down to
+ * fp32.  Queries and weights enter the products in 22 bits (of a head's largest
+ * element or weight) or more; over a BF16 cache in 24 for dtype F32 and 16 for F16
+ * and BF16 (which hold such a query whole).  A capped score is off by
+ * softcap 2^-21 at most where softcap <= 64 and dtype is not F32, else by fp32's
+ * roundings.  Over I8 and INT4G32 caches a weight times its V scale is held down to
  * 2^-38 of the largest V scale met so far, whose position may have little weight.
  * At most 2^30 tiles of 16
  * positions by 16 query heads of a cached head in all, as the table's sizes

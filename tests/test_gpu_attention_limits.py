@@ -123,3 +123,20 @@ def test_weights_of_fp32_callers_keep_their_bits(made, cache, dim, kv_heads, gro
     want = torch.sigmoid(s)
     rel = 6 * R.U + 2.0 ** -22 + 2.0 ** -23 + 12 * R.U + (2.0 ** -21 * math.log(2) if cache == "f16" else 0)
     check(out[:, :, 0], want, want * rel)
+
+
+@pytest.mark.parametrize("cap", [5.0, 30.0, 64.0, 65.0])
+@pytest.mark.parametrize("cache,unit", [("bf16", 1.0), ("f16", 1.0), ("i8", 127.0), ("int4g32", 7.0)])
+def test_capped_scores_of_fp32_callers(made, cache, unit, cap):
+    """One position: the log of the sum is the capped score.  Relative roundings: the score 6 steps and its quotient by the
+    cap 2 (2 log 2 of it is tanh's argument: 2 more), none of them larger in the tangent; tanh 2^-22; the products with the
+    cap and log 2 and their constants 4."""
+    lens = [1] * 40
+    c = one_hot(cache, lens, 1, 64, 16, lambda p: 9, unit, lambda p: 0, lambda p: unit)
+    q = torch.zeros(40, 4, 64)
+    q[:, :, 9] = (torch.randn(40, 4, generator=gen(3)) * 4).bfloat16().float()
+    a, q, out, lse = attend(made, c, lens, 4, "f32", q=q, scale=0.25 / unit, softcap=cap)
+    # (scale is an fp32 number for the library)
+    s = q[:, :, 9].double() * unit * float(torch.tensor(0.25 / unit, dtype=torch.float32))
+    want = cap * torch.tanh(s / cap)
+    check(lse, want, want.abs() * (6 + 2 + 2 + 4 + 4) * R.U + 2.0 ** -149)
