@@ -57,16 +57,6 @@ class pi_attn_desc(ctypes.Structure):
                 ("window", ctypes.c_int), ("device", ctypes.c_int)]
 
 
-class _kv_cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int)]
-
-
-class _kv_table(ctypes.Structure):
-    _fields_ = [("pages", ctypes.c_void_p), ("n_seqs", ctypes.c_int), ("width", ctypes.c_int),
-                ("stride", ctypes.c_int64)]
-
-
 _lib = None
 
 
@@ -374,8 +364,7 @@ def pi_attn_create(n_heads, n_kv_heads, head_dim, cache_dtype="bf16", page_size=
     _native()
     h = ctypes.c_void_p()
     _check(lib().pi_attn_create(ctypes.byref(desc), ctypes.byref(h)), w)
-    _desc[h.value] = {"kind": "attention", "heads": n_heads, "kv_heads": n_kv_heads, "dim": head_dim, "code": code,
-                      "page": page_size, "layout": layout, "device": device,
+    _desc[h.value] = {"kind": "attention", "device": device, "format": (code, page_size, KV_LAYOUT[layout]),
                       "layer": (h.value, n_heads, n_kv_heads, head_dim, device)}
     return h.value
 
@@ -393,42 +382,28 @@ def pi_attn_sync(a, stream=None) -> int:
 class pi_kv_cache:
     """The tensors of one layer's cache: k and v [pages, kv heads, page size, row] ("hnd") or [pages, page size, kv
     heads, row] ("nhd") with row = head_dim values (float16, bfloat16, int8) or head_dim/2 bytes (int4g32: uint8);
-    scales without the row (float32) for int8, with head_dim/32 float16 for int4g32."""
+    scales without the row (float32) for int8, with head_dim/32 float16 for int4g32.  The four tensors are the cache's for
+    good; their memory and shapes are taken, and checked against the handle's format, at each call."""
+
+    __slots__ = ("_tensors", "_of", "_arg")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.c = _kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
-        self.address = ctypes.addressof(self.c)
-        self.checked = None
+        self._tensors, self._of, self._arg = (k, v, k_scale, v_scale), None, None
+
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
 
-def _cache_arg(cache, d, where):
-    if cache.checked is not d:
-        import torch
-        row, dt, scale = {1: (d["dim"], torch.float16, None), 2: (d["dim"], torch.bfloat16, None),
-                          4: (d["dim"], torch.int8, ((), torch.float32)),
-                          3: (d["dim"] // 2, torch.uint8, ((d["dim"] // 32,), torch.float16))}[d["code"]]
-        lead = (cache.k.shape[0], d["kv_heads"], d["page"]) if d["layout"] == "hnd" else \
-            (cache.k.shape[0], d["page"], d["kv_heads"])
-        for name in ("k", "v"):
-            t, s = getattr(cache, name), getattr(cache, name + "_scale")
-            if t.shape != (*lead, row) or t.dtype != dt or not t.is_contiguous():
-                _bad(where, f"cache {name} must be contiguous {dt} {[*lead, row]}")
-            if scale is None:
-                if s is not None:
-                    _bad(where, f"a cache of {dt} has no scales")
-            elif s is None or s.shape != (*lead, *scale[0]) or s.dtype != scale[1] or not s.is_contiguous():
-                _bad(where, f"cache {name}_scale must be contiguous {scale[1]} {[*lead, *scale[0]]}")
-            if t.get_device() != d["device"] or (s is not None and s.get_device() != d["device"]):
-                _bad(where, f"cache {name} is not on cuda:{d['device']}")
-        cache.checked = d
-    return cache.address
+def _cache_arg(cache, d):
+    """The tuple that the native part takes: the format that the handle expects, and the tensors."""
+    if cache._of is not d:
+        cache._of, cache._arg = d, (*d["format"], *cache._tensors)
+    return cache._arg
 
 
 def pi_kv_append(a, cache, table, pos, q, k, v, q_out, seq=None, q_norm=None, k_norm=None, stream=None):
     """q, q_out [tokens, heads, dim], k and v [tokens, kv heads, dim]; `pos` (and `seq`) int32 [tokens]."""
     d = _handle_desc(a, "attention", "pi_kv_append")
-    got = _native_module.append(d["layer"], _cache_arg(cache, d, "pi_kv_append"), table, pos, q, k, v, q_out, seq, q_norm, k_norm,
+    got = _native_module.append(d["layer"], _cache_arg(cache, d), table, pos, q, k, v, q_out, seq, q_norm, k_norm,
                                 stream if stream is None else _stream_arg(stream))
     if got is not None:
         _fail(got, "pi_kv_append")
@@ -437,7 +412,7 @@ def pi_kv_append(a, cache, table, pos, q, k, v, q_out, seq=None, q_norm=None, k_
 def pi_kv_read(a, cache, table, pos, k_out, v_out, seq=None, stream=None):
     """k_out and v_out: contiguous [tokens, kv heads, dim] of one type."""
     d = _handle_desc(a, "attention", "pi_kv_read")
-    got = _native_module.read(d["layer"], _cache_arg(cache, d, "pi_kv_read"), table, pos, k_out, v_out, seq,
+    got = _native_module.read(d["layer"], _cache_arg(cache, d), table, pos, k_out, v_out, seq,
                               stream if stream is None else _stream_arg(stream))
     if got is not None:
         _fail(got, "pi_kv_read")
@@ -446,7 +421,7 @@ def pi_kv_read(a, cache, table, pos, k_out, v_out, seq=None, stream=None):
 def pi_paged_attention(a, cache, table, lens, q, out, lse=None, stream=None):
     """q and out [sequences, heads, dim]; `lens` int32 [sequences]; `lse` float32 [sequences, heads] or None."""
     d = _handle_desc(a, "attention", "pi_paged_attention")
-    got = _native_module.attend(d["layer"], _cache_arg(cache, d, "pi_paged_attention"), table, lens, q, out, lse,
+    got = _native_module.attend(d["layer"], _cache_arg(cache, d), table, lens, q, out, lse,
                                 stream if stream is None else _stream_arg(stream))
     if got is not None:
         _fail(got, "pi_paged_attention")

@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
+#include <cstdint>
 #include <cstdio>
 #include <exception>
 #include <string>
@@ -71,7 +72,8 @@ const at::Tensor &tensor(PyObject *o, const char *name, int device)
 {
     if (!THPVariable_Check(o)) refuse("%s must be a tensor", name);
     const at::Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.get_device() != device) refuse("%s is not on cuda:%d", name, device);
+    const at::Device on = t.device();
+    if (!on.is_cuda() || on.index() != device) refuse("%s is not on cuda:%d", name, device);
     if (t.layout() != at::kStrided) refuse("%s must be a strided tensor", name);
     return t;
 }
@@ -159,6 +161,43 @@ pi_kv_table table_of(PyObject *o, int device)
     return r;
 }
 
+// The cache's tensors as they are now, of the handle's format: (dtype, page_size, layout, k, v, k_scale, v_scale).
+pi_kv_cache cache_of(PyObject *o, const Layer &l)
+{
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 7) refuse("not a cache");
+    const long long code = integer(PyTuple_GET_ITEM(o, 0)), page = integer(PyTuple_GET_ITEM(o, 1)), layout = integer(PyTuple_GET_ITEM(o, 2));
+    const int64_t rows[2] = {layout == PI_KV_HND ? l.kv_heads : page, layout == PI_KV_HND ? page : l.kv_heads};
+    const bool scaled = code == PI_I8 || code == PI_INT4G32;
+    const int64_t row = code == PI_INT4G32 ? l.dim / 2 : l.dim, groups = code == PI_INT4G32 ? l.dim / 32 : 0;
+    const at::ScalarType type = code == PI_F16 ? at::kHalf : code == PI_BF16 ? at::kBFloat16 : code == PI_I8 ? at::kChar : at::kByte;
+    // pages x rows x `last` values (0: without the last axis)
+    auto data = [&](PyObject *t, const char *name, at::ScalarType want, int64_t last, int64_t &pages) {
+        const at::Tensor &x = tensor(t, name, l.device);
+        if (x.scalar_type() != want) refuse("%s must be %s", name, c10::toString(want));
+        const at::IntArrayRef n = x.sizes();
+        if (n.size() != (last ? 4u : 3u) || n[1] != rows[0] || n[2] != rows[1] || (last && n[3] != last) || !x.is_contiguous())
+            refuse(last ? "%s must be contiguous [pages, %lld, %lld, %lld]" : "%s must be contiguous [pages, %lld, %lld]", name,
+                   (long long)rows[0], (long long)rows[1], (long long)last);
+        if (pages < 0) pages = n[0];
+        if (n[0] != pages || pages > INT32_MAX) refuse("the cache's tensors must have the same number of pages (below 2^31)");
+        return x.data_ptr();
+    };
+    int64_t pages = -1;
+    pi_kv_cache c{};
+    PyObject *const *t = &PyTuple_GET_ITEM(o, 3);
+    c.k = data(t[0], "cache k", type, row, pages);
+    c.v = data(t[1], "cache v", type, row, pages);
+    if (scaled != (t[2] != Py_None) || scaled != (t[3] != Py_None))
+        refuse("a cache of %s has %s", c10::toString(type), scaled ? "k_scale and v_scale" : "no scales");
+    if (scaled) {
+        const at::ScalarType scale = code == PI_I8 ? at::kFloat : at::kHalf;
+        c.k_scale = data(t[2], "cache k_scale", scale, groups, pages);
+        c.v_scale = data(t[3], "cache v_scale", scale, groups, pages);
+    }
+    c.n_pages = int(pages);
+    return c;
+}
+
 int token_count(const at::Tensor &pos)
 {
     if (pos.dim() != 1 || pos.size(0) > (1 << 30)) refuse("pos must be contiguous [tokens]");
@@ -201,8 +240,8 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t nargs)
     return guarded([&]() -> pi_status {
         arguments(nargs, 12);
         const Layer l(v[0]);
-        const pi_kv_cache *cache = static_cast<const pi_kv_cache *>(address(v[1]));
         const pi_kv_table table = table_of(v[2], l.device);
+        const pi_kv_cache cache = cache_of(v[1], l);
         const at::Tensor &pos = tensor(v[3], "pos", l.device);
         const int tokens = token_count(pos);
         const int32_t *pp = ints(pos, "pos", tokens), *sp = v[8] == Py_None ? nullptr : ints(tensor(v[8], "seq", l.device), "seq", tokens);
@@ -214,7 +253,7 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t nargs)
         const int64_t qs = token_rows(q, "q", tokens, l.heads, l.dim), ks = token_rows(k, "k", tokens, l.kv_heads, l.dim),
                       vs = token_rows(w, "v", tokens, l.kv_heads, l.dim), os = token_rows(o, "q_out", tokens, l.heads, l.dim);
         const float *qn = norm_weight(v[9], "q_norm", l.device, int(l.dim)), *kn = norm_weight(v[10], "k_norm", l.device, int(l.dim));
-        return unlocked(f_append, l.a, cache, &table, tokens, sp, pp, pi_dtype(code), (const void *)q.data_ptr(), qs,
+        return unlocked(f_append, l.a, &cache, &table, tokens, sp, pp, pi_dtype(code), (const void *)q.data_ptr(), qs,
                         (const void *)k.data_ptr(), ks, (const void *)w.data_ptr(), vs, qn, kn, o.data_ptr(), os,
                         stream_of(v[11], l.device));
     });
@@ -226,8 +265,8 @@ PyObject *read(PyObject *, PyObject *const *v, Py_ssize_t nargs)
     return guarded([&]() -> pi_status {
         arguments(nargs, 8);
         const Layer l(v[0]);
-        const pi_kv_cache *cache = static_cast<const pi_kv_cache *>(address(v[1]));
         const pi_kv_table table = table_of(v[2], l.device);
+        const pi_kv_cache cache = cache_of(v[1], l);
         const at::Tensor &pos = tensor(v[3], "pos", l.device);
         const int tokens = token_count(pos);
         const int32_t *pp = ints(pos, "pos", tokens), *sp = v[6] == Py_None ? nullptr : ints(tensor(v[6], "seq", l.device), "seq", tokens);
@@ -237,7 +276,7 @@ PyObject *read(PyObject *, PyObject *const *v, Py_ssize_t nargs)
         token_rows(w, "v_out", tokens, l.kv_heads, l.dim);
         if (!k.is_contiguous() || !w.is_contiguous() || w.scalar_type() != k.scalar_type())
             refuse("k_out and v_out must be contiguous, both of one type");
-        return unlocked(f_read, l.a, cache, &table, tokens, sp, pp, pi_dtype(code), k.data_ptr(), w.data_ptr(), stream_of(v[7], l.device));
+        return unlocked(f_read, l.a, &cache, &table, tokens, sp, pp, pi_dtype(code), k.data_ptr(), w.data_ptr(), stream_of(v[7], l.device));
     });
 }
 
@@ -247,8 +286,8 @@ PyObject *attend(PyObject *, PyObject *const *v, Py_ssize_t nargs)
     return guarded([&]() -> pi_status {
         arguments(nargs, 8);
         const Layer l(v[0]);
-        const pi_kv_cache *cache = static_cast<const pi_kv_cache *>(address(v[1]));
         const pi_kv_table table = table_of(v[2], l.device);
+        const pi_kv_cache cache = cache_of(v[1], l);
         const int32_t *lens = ints(tensor(v[3], "lens", l.device), "lens", table.n_seqs);
         const at::Tensor &q = tensor(v[4], "q", l.device), &o = tensor(v[5], "out", l.device);
         const int code = float_code(q, "q");
@@ -261,7 +300,7 @@ PyObject *attend(PyObject *, PyObject *const *v, Py_ssize_t nargs)
                 refuse("lse must be contiguous float32 [sequences, heads]");
             lse = static_cast<float *>(e.data_ptr());
         }
-        return unlocked(f_attend, l.a, cache, &table, lens, pi_dtype(code), (const void *)q.data_ptr(), qs, o.data_ptr(), os, lse,
+        return unlocked(f_attend, l.a, &cache, &table, lens, pi_dtype(code), (const void *)q.data_ptr(), qs, o.data_ptr(), os, lse,
                         stream_of(v[7], l.device));
     });
 }

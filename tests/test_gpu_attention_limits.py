@@ -140,3 +140,29 @@ def test_capped_scores_of_fp32_callers(made, cache, unit, cap):
     s = q[:, :, 9].double() * unit * float(torch.tensor(0.25 / unit, dtype=torch.float32))
     want = cap * torch.tanh(s / cap)
     check(lse, want, want.abs() * (6 + 2 + 2 + 4 + 4) * R.U + 2.0 ** -149)
+
+
+def test_a_cache_s_tensors_are_taken_as_they_are_at_the_call(made):
+    """A cache tensor that is given other memory or another shape after a call is used, or refused, as it then is."""
+    c = R.Cache(gen(1), [20], 2, 64, "f16", 16, spare=1).cuda()
+    other = R.Cache(gen(2), [20], 2, 64, "f16", 16, spare=1).cuda()
+    a = layer(made, 4, 2, 64, cache_dtype="f16", page_size=16)
+    pos, seq = torch.arange(20, dtype=torch.int32).cuda(), torch.zeros(20, dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros(20, 2, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+    cache, keep = cache_of(c), c.k.view(-1)
+    table = torch.tensor([[0, 2]], dtype=torch.int32, device="cuda")
+    read = lambda: B.pi_kv_read(a, cache, table, pos, k, v, seq=seq)  # noqa: E731
+    flat = lambda t: torch.cat((t[0], t[2]), 1).transpose(0, 1)[:20]  # noqa: E731  (pages 0 and 2, [positions, heads, dim])
+    read()
+    assert torch.equal(k, flat(c.k)) and torch.equal(v, flat(c.v))
+    c.k.set_(other.k)
+    read()
+    assert torch.equal(k, flat(other.k)) and torch.equal(v, flat(c.v))
+    with pytest.raises(AttributeError):
+        cache.k = c.v
+    c.k.resize_(2, 2, 16, 64)          # K of two pages, V of three
+    refused(read)
+    c.v.resize_(2, 2, 16, 64)
+    read()
+    assert B.pi_attn_sync(a) == B.PI_ERR_DEVICE_CHECK      # page 2 is none of the cache's any more
+    assert keep.numel() == 3 * 2 * 16 * 64
