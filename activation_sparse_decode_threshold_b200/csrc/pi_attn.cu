@@ -74,6 +74,13 @@ bool overlap(const void *a, long long as, int alen, int ab, const void *b, long 
     return true;
 }
 
+// Whether two buffers of na and nb bytes share one.
+bool meet(const void *a, long long na, const void *b, long long nb)
+{
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + nb && b0 < a0 + na;
+}
+
 pi_status check_device(int device, int *n_sm)
 {
     int ndev = 0;
@@ -411,6 +418,14 @@ pi_status pi_kv_read(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_table *t
     if (st != PI_OK) return st;
     if (!aligned16(k_dev) || !aligned16(v_dev)) return fail(PI_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
     const pi_attn_desc &D = a->desc;
+    const long long bytes = (long long)n_tokens * D.n_kv_heads * D.head_dim * bytes_of(dtype), rows = (long long)cache->n_pages * p.c.page_rows;
+    if (meet(k_dev, bytes, v_dev, bytes)) return fail(PI_ERR_INVALID_ARG, "k and v overlap");
+    const long long row = D.cache_dtype == PI_I8 ? D.head_dim : D.cache_dtype == PI_INT4G32 ? D.head_dim / 2 : 2 * D.head_dim;
+    const long long scale = D.cache_dtype == PI_I8 ? 4 : D.cache_dtype == PI_INT4G32 ? D.head_dim / 16 : 0;
+    for (const void *out : {k_dev, v_dev})
+        if (meet(out, bytes, cache->k, rows * row) || meet(out, bytes, cache->v, rows * row) ||
+            (scale && (meet(out, bytes, cache->k_scale, rows * scale) || meet(out, bytes, cache->v_scale, rows * scale))))
+            return fail(PI_ERR_INVALID_ARG, "k or v overlaps the cache");
     OnDevice on(D.device);
     PI_CUDA(on.status, "cudaSetDevice");
     p.kv_heads = D.n_kv_heads;

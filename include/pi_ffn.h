@@ -364,7 +364,9 @@ PI_API pi_status pi_predict_noalloc(int d_model, int d_ff, int rank, pi_dtype pr
  * written at each call).  Conventions as above.  Calls restore the current
  * device before they return; each runs on its handle's device, which the
  * stream has to belong to.  No call allocates device memory except the two
- * create calls, so all others may be captured into CUDA graphs.
+ * create calls, so all others may be captured into CUDA graphs.  Where a call does
+ * not say that two of its buffers may be one, nothing that it writes may overlap
+ * anything else that it takes (the checks find the likely cases).
  */
 
 /* One INT4G32 matrix W, n_rows x n_cols (n_cols a multiple of 32), for products
@@ -481,7 +483,8 @@ PI_API pi_status pi_kv_append(pi_attn_t a, const pi_kv_cache *cache, const pi_kv
 /* Rows of the cache as values: k_dev and v_dev [dtype], n_tokens x n_kv_heads x
  * head_dim, 16-byte aligned, row t holding position pos_dev[t] of sequence
  * seq_dev[t] (NULL: t); rows of negative positions are left as they were.
- * Any row may be read any number of times. */
+ * Any row may be read any number of times.  k and v must overlap neither each
+ * other nor the cache. */
 PI_API pi_status pi_kv_read(pi_attn_t a, const pi_kv_cache *cache, const pi_kv_table *table, int n_tokens,
                             const int32_t *seq_dev, const int32_t *pos_dev, pi_dtype dtype, void *k_dev,
                             void *v_dev, void *stream);

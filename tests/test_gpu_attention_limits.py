@@ -166,3 +166,25 @@ def test_a_cache_s_tensors_are_taken_as_they_are_at_the_call(made):
     read()
     assert B.pi_attn_sync(a) == B.PI_ERR_DEVICE_CHECK      # page 2 is none of the cache's any more
     assert keep.numel() == 3 * 2 * 16 * 64
+
+
+def test_read_into_overlapping_buffers_is_refused(made):
+    """K's and V's rows must not share memory, with each other or with the cache."""
+    for kind in ("f16", "i8", "int4g32"):
+        c = R.Cache(gen(3), [20, 20], 2, 64, kind, 16).cuda()
+        a, cache = layer(made, 4, 2, 64, cache_dtype=kind, page_size=16), cache_of(c)
+        pos = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+        read = lambda k, v: B.pi_kv_read(a, cache, c.table_dev, pos, k, v)  # noqa: E731
+        both = torch.zeros(4, 2, 64, dtype=torch.float16, device="cuda")
+        read(both[:2], both[2:])                                           # side by side is fine
+        assert torch.equal(both[1, :, :8].cpu(), c.rows("k", 1, 2, 3)[0, :, :8].half())
+        keep = both.clone()
+        refused(lambda: read(both[:2], both[:2]))
+        refused(lambda: read(both[:2], both[1:3]))
+        refused(lambda: read(both[1:3], both[:2]))
+        for t in (c.k, c.v, c.k_scale, c.v_scale):
+            if t is not None:
+                into = t.view(-1).view(torch.float16)
+                refused(lambda: read(both[:2], into[:256].view(2, 2, 64)))
+                refused(lambda: read(into[-256:].view(2, 2, 64), both[:2]))
+        assert torch.equal(both, keep) and B.pi_attn_sync(a) == B.PI_OK
