@@ -1,5 +1,7 @@
 """Build libpi_ffn.so (sm_100a) in-tree with nvcc, and _pi_torch.so, the
-binding's native part, with g++ against torch's headers.
+binding's native part, with g++ against torch's headers.  The library needs
+nothing of torch: where torch is not installed it is built alone.  The native
+part is built again when torch or Python is another than it was built for.
 
 Usage: python -m activation_sparse_decode_threshold_b200.build [--force] [--verbose]
 """
@@ -9,7 +11,9 @@ import argparse
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from importlib import metadata
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libpi_ffn.so")
 EXT = os.path.join(HERE, "_pi_torch.so")
 OBJ = os.path.join(ROOT, "_build")
+EXT_FOR = os.path.join(OBJ, "pi_torch.for")   # what the native part was built for
 SOURCES = ["pi_decode_f16.cu", "pi_decode_bf16.cu", "pi_decode_i4f16.cu", "pi_decode_i4bf16.cu",
            "pi_decode_f16i8.cu", "pi_decode_bf16i8.cu", "pi_decode_i4i8.cu",
            "pi_decode_f32.cu", "pi_host.cu", "pi_decode.cu", "pi_repack.cu", "pi_prefill.cu", "pi_noalloc.cu", "pi_batch.cu",
@@ -43,8 +48,23 @@ def _deps_newer(target: str, sources: list[str]) -> bool:
     return False
 
 
+def _ext_target() -> str | None:
+    """What the native part's binary interface depends on (torch is not imported for it); None without torch."""
+    try:
+        return f"torch {metadata.version('torch')} python {sysconfig.get_config_var('SOABI')}\n"
+    except metadata.PackageNotFoundError:
+        return None
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _ext_cmd(src: str) -> list[str]:
-    import sysconfig
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
@@ -81,22 +101,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0 or verbose or ptxas_info:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}")
 
-    ext_src = os.path.join(CSRC, "pi_torch.cpp")
-    ext_new = force or _deps_newer(EXT, [ext_src, os.path.join(ROOT, "include", "pi_ffn.h")])
-    if ext_new:
-        jobs.append(_ext_cmd(ext_src))
+    def library():
+        with ThreadPoolExecutor(max_workers=min(os.cpu_count() or 4, max(1, len(jobs)))) as ex:
+            list(ex.map(run, jobs))
+        if force or jobs or not os.path.exists(OUT):
+            run([nvcc, *ARCH, "-shared", "-o", OUT + ".tmp", *objs, "-lcudart"])
+            os.replace(OUT + ".tmp", OUT)
 
-    with ThreadPoolExecutor(max_workers=min(os.cpu_count() or 4, max(1, len(jobs)))) as ex:
-        list(ex.map(run, jobs))
-    if ext_new:
-        os.replace(EXT + ".tmp", EXT)
-        jobs.pop()
-    if force or jobs or not os.path.exists(OUT):
-        cmd = [nvcc, *ARCH, "-shared", "-o", OUT + ".tmp", *objs, "-lcudart"]
-        run(cmd)
-        os.replace(OUT + ".tmp", OUT)
+    def native_part():
+        target = _ext_target()
+        if target is None:
+            sys.stderr.write("torch is not installed: the binding's native part is not built\n")
+            return
+        ext_src = os.path.join(CSRC, "pi_torch.cpp")
+        if force or _read(EXT_FOR) != target or _deps_newer(EXT, [ext_src, os.path.join(ROOT, "include", "pi_ffn.h")]):
+            run(_ext_cmd(ext_src))
+            os.replace(EXT + ".tmp", EXT)
+            with open(EXT_FOR, "w") as f:
+                f.write(target)
+
+    with ThreadPoolExecutor(max_workers=2) as ex:
+        parts = [ex.submit(library), ex.submit(native_part)]
+    for part in parts:   # the library first: it is there whatever becomes of the native part
+        part.result()
     return OUT
 
 
