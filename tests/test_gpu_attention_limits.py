@@ -1,5 +1,5 @@
 """The attention half of a decode layer at the limits of its numbers: the largest
-values, few rounded steps, long exact sums.  Definitions and roundings: attn_ref.py."""
+values, few rounded steps, long exact sums; and what stands beside a call.  Definitions and roundings: attn_ref.py."""
 import math
 
 import pytest
@@ -8,6 +8,7 @@ import torch
 import attn_ref as R
 from activation_sparse_decode_threshold_b200 import binding as B
 from test_gpu_attention import attend, cache_of, check, gen, layer, made, matrix, refused  # noqa: F401
+from test_gpu_attention_layer import Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +189,77 @@ def test_read_into_overlapping_buffers_is_refused(made):
                 refused(lambda: read(both[:2], into[:256].view(2, 2, 64)))
                 refused(lambda: read(into[-256:].view(2, 2, 64), both[:2]))
         assert torch.equal(both, keep) and B.pi_attn_sync(a) == B.PI_OK
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,k,tokens", [(8, 131072, 1), (16, 131072, 32), (19, 32768, 32), (300, 8192, 13), (2500, 320, 1),
+                                        (33, 4128, 24), (50, 14336, 8)])
+def test_matvec_sums_of_whole_numbers_are_exact(made, dt, n, k, tokens):
+    """x in -3 .. 3, scales 1/2 and 1: every sum is a multiple of 1/2 below 2^23, which fp32 holds, so that a group lost,
+    doubled or of another row shows at any length."""
+    g = gen(n + k)
+    q = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8)
+    s = torch.where(torch.rand(n, k // 32, generator=g) < 0.5, 0.5, 1.0).half()
+    x = torch.randint(-3, 4, (tokens, k), generator=g).to(R.DT[dt])
+    add = torch.randint(-100, 101, (tokens, n), generator=g).float()
+    w = R.decode(q, s, "int4g32")
+    want = x.double() @ w.t()
+    assert (x.double().abs() @ w.abs().t()).max() + 100 < 2 ** 23
+    m, xd, y = matrix(made, q, s), x.cuda(), torch.full((tokens, n), 0.25, device="cuda")
+    B.pi_int4_matvec(m, xd, y)
+    assert torch.equal(y.cpu().double(), want)
+    B.pi_int4_matvec(m, xd, y, add=add.cuda())
+    assert torch.equal(y.cpu().double(), want + add)
+
+
+@pytest.mark.parametrize("lens", [[1, 3000, 0, 5, 1700], [2048, 2049] * 3, [1] * 40 + [900]])
+@pytest.mark.parametrize("cache,heads,kv_heads,dim", [("bf16", 8, 8, 64), ("int4g32", 8, 2, 128), ("i8", 16, 1, 64)])
+def test_attention_of_a_batch_is_that_of_each_alone(made, lens, cache, heads, kv_heads, dim):
+    """The same values, within both calls' bounds, whatever stands beside a sequence."""
+    c = R.Cache(gen(len(lens)), lens, kv_heads, dim, cache, 16).cuda()
+    a, q, out, lse = attend(made, c, lens, heads, "f16")
+    for s in [i for i in range(len(lens)) if i < 6 or i > 38]:
+        o1, l1 = torch.full_like(out[:1], 5.0), torch.full_like(lse[:1], 5.0)
+        n1 = torch.tensor(lens[s:s + 1], dtype=torch.int32, device="cuda")
+        B.pi_paged_attention(a, cache_of(c), c.table_dev[s:s + 1], n1, q[s:s + 1].cuda(), o1, lse=l1)
+        want, l, bound, lb = R.attention(c, s, lens[s], q[s])
+        if lens[s] == 0:
+            assert torch.equal(o1[0], out[s]) and torch.equal(l1[0], lse[s])
+            continue
+        check(o1[0], out[s].cpu().double(), 2 * (bound + R.half_step(want.abs() + bound, out.dtype)), f"out of sequence {s}")
+        check(l1[0], lse[s].cpu().double(), 2 * lb, f"lse of sequence {s}")
+
+
+class LayerWithLse(Layer):
+    """A layer whose attention gives the log of its sums too."""
+
+    def step(self, a, r, pos, lens):
+        h, k, d = self.heads, self.kv_heads, self.dim
+        part = lambda i, n: self.qkv[:, i * d:(i + n) * d].unflatten(1, (n, d))  # noqa: E731
+        self.logs = torch.full((r.shape[0], h), 3.0, device="cuda")
+        B.pi_int4_matvec(self.m[0], r, self.qkv, norm_eps=1e-6)
+        B.pi_kv_append(a, self.cache, self.c.table_dev, pos, part(0, h), part(h, k), part(h + k, k), self.q,
+                       q_norm=self.norms[0], k_norm=self.norms[1])
+        B.pi_paged_attention(a, self.cache, self.c.table_dev, lens, self.q, self.o.unflatten(1, (h, d)), lse=self.logs)
+        B.pi_int4_matvec(self.m[1], self.o, r, add=r)
+
+    def lse(self, lens, q):
+        return self.logs
+
+
+@pytest.mark.parametrize("cache,io,tokens", [("bf16", "bf16", 3), ("f16", "f16", 1), ("i8", "f16", 5), ("int4g32", "f16", 2),
+                                             ("bf16", "f32", 2)])
+def test_a_layer_s_steps_with_the_logs_of_the_sums(made, cache, io, tokens):
+    """Steps of growing texts, every stage on the inputs that it really had, the logs of the sums among them."""
+    g = gen(tokens)
+    heads, kv_heads, dim, theta = 6, 2, 64, 10000.0
+    lens = [29 + 7 * s for s in range(tokens)]
+    a = layer(made, heads, kv_heads, dim, cache_dtype=cache, page_size=16, rotary_dim=dim, rope_theta=theta, norm_eps=1e-6)
+    la = LayerWithLse(made, g, 512, heads, kv_heads, dim, cache, 16, [n + 4 for n in lens], tokens, io)
+    r = torch.randn(tokens, 512, generator=g).cuda()
+    for step in range(3):
+        now = [n + step for n in lens]
+        before = r.cpu()
+        la.step(a, r, torch.tensor(now, dtype=torch.int32).cuda(), torch.tensor([n + 1 for n in now], dtype=torch.int32).cuda())
+        assert B.pi_attn_sync(a) == B.PI_OK
+        la.check(before, r, now, [n + 1 for n in now], theta)
