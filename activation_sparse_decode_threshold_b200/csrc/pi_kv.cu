@@ -339,7 +339,7 @@ cudaError_t append_launch(const AppendParams &p, cudaStream_t st, int ctas)
 }
 
 // Few tokens: 4 elements to a lane, the shorter way (one token of 32 + 2 x 8 heads of 128 into 4 bits: 3.5 us, with 8
-// elements 4.3).  Many: 8, in fewer instructions (512 tokens 9.9 us, with 4 elements 13.1).  Both are even at 64 to 130.
+// elements 4.3).  Many: 8, in fewer instructions (512 tokens 9.8 us, with 4 elements 13).  Both are even at 64 to 130.
 template <int D>
 cudaError_t append_by_tokens(const AppendParams &p, cudaStream_t st)
 {

@@ -21,11 +21,11 @@
 // head's two columns meet in one lane.  Scales of quantised rows are applied in
 // fp32, to the scores (K) and to the weights (V).
 //
-// Measured: 32 ragged texts of bf16 (525 MB) 103 us, 5.1 TB/s; 32768 positions of
-// 4 bits 23.9 us, of which 12 are its chunks' instructions and 10 the way to the
+// Measured: 32 ragged texts of bf16 (525 MB) 104 us, 5.0 TB/s; 32768 positions of
+// 4 bits 24.0 us, of which 12 are its chunks' instructions and 10 the way to the
 // first product and from the last to the result; 16 texts of 8 bits in a window,
-// 16 queries to a cached head, 36.8 us, bound by instructions.  Taking 8 instead
-// of 16 heads at a time, with 12 instead of 8 warps, made the last 39.2 us.
+// 16 queries to a cached head, 37.1 us, bound by instructions (taking 8 instead of
+// 16 heads at a time, with 12 instead of 8 warps, makes it 6% longer).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,8 +36,8 @@
 namespace pi {
 namespace {
 
-// What the start of an item costs, in chunks (8-bit window of 16 ragged texts: 1 44.6 us, 2 37.7, 4 37.2; 200 positions:
-// 8.5, 8.4, 10.7).
+// What the start of an item costs, in chunks (8-bit window of 16 ragged texts: with 1 18% longer, with 4 1% shorter; 200
+// positions: 1% and 27% longer).
 constexpr int kStart = 2;
 constexpr int kSlots = 32;            // partial results of a CTA's warps, at most (2 for each)
 
@@ -380,7 +380,9 @@ __global__ void __launch_bounds__(32 * Cfg<FMT, D, NB, WIDE>::kWarps, 1) k_paged
 
     // ---- this warp's share ---------------------------------------------------
     int ctas = min((total + W - 1) / W, int(gridDim.x));   // at least a unit for each warp
-    if (n == 1 && 4 * items <= int(gridDim.x)) ctas = max(ctas / items, 1) * items;   // no CTA with parts of two items
+    // One text: no CTA with parts of two items, which saves joins (bf16, 32 cached heads of 128: 200 positions 8.6 us instead
+    // of 10.9, 2000 15.0, 16.9, 8000 33.9, 34.4) and leaves SMs idle (128 of 148 work: 32768 positions 104.9 us, 100.0).
+    if (n == 1 && 4 * items <= int(gridDim.x)) ctas = max(ctas / items, 1) * items;
     if (int(blockIdx.x) >= ctas) return;
     const Shares shares(total, ctas);
     const int cta0 = shares.first(blockIdx.x), units = shares.first(blockIdx.x + 1) - cta0;
@@ -1223,6 +1225,7 @@ cudaError_t attn_setup()
         for (int dim : {64, 128})
             for (int group : {4, 8, 16})
                 for (int dt : {int(kF16), int(kF32)}) {
+                    if (dt == kF32 && fmt != kBF16) continue;   // (other formats have one kernel for all callers)
                     p.c.fmt = fmt;
                     p.dim = dim;
                     p.group = group;
