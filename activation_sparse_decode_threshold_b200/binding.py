@@ -385,19 +385,21 @@ class pi_kv_cache:
     scales without the row (float32) for int8, with head_dim/32 float16 for int4g32.  The four tensors are the cache's for
     good; their memory and shapes are taken, and checked against the handle's format, at each call."""
 
-    __slots__ = ("_tensors", "_of", "_arg")
+    __slots__ = ("_tensors", "_last")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        self._tensors, self._of, self._arg = (k, v, k_scale, v_scale), None, None
+        self._tensors, self._last = (k, v, k_scale, v_scale), (None, None)
 
     k, v, k_scale, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
 
 def _cache_arg(cache, d):
     """The tuple that the native part takes: the format that the handle expects, and the tensors."""
-    if cache._of is not d:
-        cache._of, cache._arg = d, (*d["format"], *cache._tensors)
-    return cache._arg
+    of, arg = cache._last
+    if of is not d:
+        arg = (*d["format"], *cache._tensors)
+        cache._last = d, arg   # (both at once: threads may use a cache with handles of their own)
+    return arg
 
 
 def pi_kv_append(a, cache, table, pos, q, k, v, q_out, seq=None, q_norm=None, k_norm=None, stream=None):

@@ -390,13 +390,13 @@ PI_API void pi_int4_destroy(pi_int4_t m);
  *   add_dev  NULL, or rows like y's (may be y_dev itself: y += W f(x))
  *   y_dev    n_tokens rows of n_rows values [y_dtype], y_stride elements apart
  * Types F32, F16 or BF16.  Products are exact (x in parts that hold all its
- * bits), sums are fp32 (of 1/256 of the terms for F32 and BF16 x, so that x up to
- * its type's largest number is fine while the sums of s x stay below that; the
- * norm's factor comes last, and its squares may leave fp32's range), y is
- * rounded once.  Each token's row comes from that
- * token alone (the order of its sums, and so its last bits, may differ with
- * n_tokens), the result is deterministic, and calls on several streams may
- * overlap.  x must not overlap y, nor add overlap y unless both are the same
+ * bits), sums are fp32, y is rounded once.  For F32 and BF16 x the sums are taken
+ * of 1/256 of the terms, so that x may be as large as its type allows while the
+ * sums of s x stay in range (a y below 2^-110 may lose its lowest bits); the norm's
+ * factor comes last, and its squares may leave fp32's range.  Each token's row
+ * comes from that token alone (the order of its sums, and so its last bits, may
+ * differ with n_tokens), the result is deterministic, and calls on several streams
+ * may overlap.  x must not overlap y, nor add overlap y unless both are the same
  * rows.  Errors: PI_ERR_INVALID_ARG, PI_ERR_CUDA. */
 PI_API pi_status pi_int4_matvec(pi_int4_t m, int n_tokens, pi_dtype x_dtype, const void *x_dev, int64_t x_stride,
                                 const void *add_dev, pi_dtype y_dtype, void *y_dev, int64_t y_stride,

@@ -263,3 +263,28 @@ def test_a_layer_s_steps_with_the_logs_of_the_sums(made, cache, io, tokens):
         la.step(a, r, torch.tensor(now, dtype=torch.int32).cuda(), torch.tensor([n + 1 for n in now], dtype=torch.int32).cuda())
         assert B.pi_attn_sync(a) == B.PI_OK
         la.check(before, r, now, [n + 1 for n in now], theta)
+
+
+@pytest.mark.parametrize("dim,kv_heads,group", [(64, 8, 1), (128, 4, 4), (64, 2, 8), (128, 1, 16), (64, 1, 16)])
+@pytest.mark.parametrize("lens,window", [([4000], 0), ([1, 3000, 0, 5, 1700], 700), ([700, 2, 0, 130] * 10, 0)])
+def test_attention_of_fp32_callers_over_bf16(made, lens, window, dim, kv_heads, group):
+    """Texts that warps and CTAs share, empty ones and many, in the form that fp32 callers over a bf16 cache have."""
+    c = R.Cache(gen(dim + group), lens, kv_heads, dim, "bf16", 16).cuda()
+    a, q, out, lse = attend(made, c, lens, kv_heads * group, "f32", window=window)
+    assert B.pi_attn_sync(a) == B.PI_OK
+    for s in [i for i in range(len(lens)) if i < 6 or i == len(lens) - 1]:
+        want, l, bound, lb = R.attention(c, s, lens[s], q[s], window=window)
+        check(out[s], want, bound + R.half_step(want.abs() + bound, torch.float32), f"out of sequence {s}")
+        if lens[s]:
+            check(lse[s], l, lb, f"lse of sequence {s}")
+        else:
+            assert (lse[s] == -math.inf).all()
+    o1, l1 = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    n, qd, cache = torch.tensor(lens, dtype=torch.int32).cuda(), q.cuda(), cache_of(c)
+    with torch.cuda.graph(graph):
+        B.pi_paged_attention(a, cache, c.table_dev, n, qd, out, lse=lse)
+    for _ in range(2):
+        out.fill_(3.0)
+        graph.replay()
+        assert torch.equal(o1, out) and torch.equal(l1, lse)
